@@ -144,6 +144,53 @@ PA_API int pa_rope_append_kv(const pa_bf16* q, pa_bf16* q_out, const pa_bf16* k,
                              int32_t num_tokens, float rope_theta, pa_bf16* k_cache,
                              pa_bf16* v_cache, const pa_cache_desc* desc, void* stream);
 
+/*
+ * 4-bit KV cache.  The Tiny-vLLM summary page ("[Hacker News 요약] ... Tiny-vLLM
+ * ...", section "향후 전망") names lower-precision data types among the things to
+ * add, with no format.  This library uses E2M1 codes (1 sign, 2 exponent, 1
+ * mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6) with one E4M3 scale per group of 16
+ * values along head_dim and one float scale gs per cache tensor.  For a group
+ * of bf16 values x:
+ *   y = float(x) * float(1/gs)             (one float product)
+ *   s = E4M3(max|y| / 6)                   (nearest even, saturating at 448)
+ *   code = E2M1(y / s)                     (nearest even, saturating at +-6; 0 where s = 0)
+ * with correctly rounded float quotients; a value reads back as code * s * gs.  A
+ * group holding a NaN reads back as NaN.
+ * A cache is a uint8 pool [N][Hkv][page], a page being Bs rows of head_dim / 2
+ * code bytes (the even dim in the low nibble) followed by head_dim / 16 rows of Bs
+ * scale bytes (the scale of group g of the page's token t at [g][t]):
+ * 9 head_dim / 16 bytes a row, against 2 head_dim in bf16.
+ * head_dim 64 or 128, block_size 8, 16, 32, 64, 128 or 256 (PA_ERR_UNSUPPORTED
+ * otherwise), any number of kv heads; caches 16-byte aligned.
+ */
+
+/* Bytes of one cache tensor (K, or V) of this geometry for a PA_KV_* type; 0 on bad arguments. */
+PA_API size_t pa_kv_cache_bytes(const pa_cache_desc* desc, int32_t kv_dtype);
+
+/* pa_append_kv into 4-bit pools: the same slots and rules (a skipped token's bytes, and every
+ * other token's, stay as they are); k_scale, v_scale: gs of each cache, positive and finite as
+ * are their reciprocals. */
+PA_API int pa_append_kv_e2m1(const pa_bf16* k, const pa_bf16* v, const int64_t* slot_mapping,
+                             int32_t num_tokens, float k_scale, float v_scale, uint8_t* k_cache,
+                             uint8_t* v_cache, const pa_cache_desc* desc, void* stream);
+
+/* pa_rope_append_kv into 4-bit pools: q is turned into q_out (q_out == q turns in place), k is
+ * turned, rounded to bf16 and that row quantized.  K rows are turned in double throughout and
+ * rounded to float, then bf16, so that a code does not depend on where it was computed; q rows
+ * as pa_rope_append_kv turns them. */
+PA_API int pa_rope_append_kv_e2m1(const pa_bf16* q, pa_bf16* q_out, const pa_bf16* k, const pa_bf16* v,
+                                  const int32_t* positions, const int64_t* slot_mapping,
+                                  int32_t num_tokens, float rope_theta, float k_scale, float v_scale,
+                                  uint8_t* k_cache, uint8_t* v_cache, const pa_cache_desc* desc,
+                                  void* stream);
+
+/* Rows of 4-bit pools read back: k[t], v[t] ([num_tokens][Hkv][D] bf16) receive slot
+ * slot_mapping[t]'s values (code * s exact, times gs in float, rounded to nearest-even bf16);
+ * zeros for a slot outside the pool. */
+PA_API int pa_gather_kv_e2m1(const uint8_t* k_cache, const uint8_t* v_cache, const int64_t* slot_mapping,
+                             int32_t num_tokens, float k_scale, float v_scale, pa_bf16* k, pa_bf16* v,
+                             const pa_cache_desc* desc, void* stream);
+
 /* ---- paged decode attention ------------------------------------------------------------ */
 #define PA_KERNEL_AUTO          0  /* the fastest built kernel for the shape                    */
 #define PA_KERNEL_SIMT          1  /* CUDA cores: plain loads, fp32 FMA                         */
@@ -164,6 +211,7 @@ PA_API int pa_rope_append_kv(const pa_bf16* q, pa_bf16* q_out, const pa_bf16* k,
 
 #define PA_KV_BF16        0   /* caches hold bf16 values                                         */
 #define PA_KV_E4M3        1   /* caches hold E4M3 codes (uint8), see pa_append_kv_e4m3           */
+#define PA_KV_E2M1        2   /* caches are 4-bit pools (uint8), see pa_append_kv_e2m1           */
 
 typedef struct pa_decode_options {
     int32_t split_tokens;  /* SIMT / TENSOR_SPLIT: 0 automatic, else tokens per KV split, a      */
@@ -174,11 +222,12 @@ typedef struct pa_decode_options {
     float rope_theta;      /* pa_append_decode only: > 0 turns q and the new K rows by RoPE at   */
                            /* position L-1 with this frequency base (see pa_rope_append_kv);    */
                            /* 0 = no rotation.  pa_decode(_ex) rejects a nonzero value.         */
-    int32_t kv_dtype;      /* PA_KV_BF16 (default) or PA_KV_E4M3: the caches are uint8 E4M3     */
+    int32_t kv_dtype;      /* PA_KV_BF16 (default); PA_KV_E4M3: the caches are uint8 E4M3       */
                            /* pools of the same [N][Hkv][Bs][D] shape (the pointers are read as */
-                           /* bytes); the whole-group tensor kernel only                        */
-    float k_scale;         /* PA_KV_E4M3: K value = code value * k_scale (> 0)                  */
-    float v_scale;         /* PA_KV_E4M3: V value = code value * v_scale (> 0)                  */
+                           /* bytes), the whole-group tensor kernel only; PA_KV_E2M1: 4-bit     */
+                           /* pools, a tensor kernel of their own                               */
+    float k_scale;         /* E4M3, E2M1: scale of the K cache tensor (> 0)                     */
+    float v_scale;         /* E4M3, E2M1: scale of the V cache tensor (> 0)                     */
 } pa_decode_options;
 
 /*
@@ -226,7 +275,14 @@ PA_API size_t pa_decode_workspace_size_ex(int32_t num_seqs, int32_t max_context_
  * rows with the same scales as it writes them; with rope_theta > 0 the new K
  * row is turned and rounded to bf16 first, and that bf16 row is quantized.
  *
- * PA_FLAG_PDL (whole-group tensor kernel only; ignored by the others): the
+ * options->kv_dtype == PA_KV_E2M1: the caches are 4-bit pools (see
+ * pa_append_kv_e2m1), for any number of kv heads; kernel PA_KERNEL_AUTO or
+ * PA_KERNEL_TENSOR (PA_ERR_UNSUPPORTED otherwise).  q is used as f16 after a
+ * power of two per row, P as f16.  pa_append_decode quantizes the new rows as
+ * pa_append_kv_e2m1 (pa_rope_append_kv_e2m1 with rope_theta > 0) does, in a
+ * launch of its own before the decode.
+ *
+ * PA_FLAG_PDL (whole-group and 4-bit tensor kernels; ignored by the others): the
  * decode kernel is launched as a programmatic dependent of the kernel before
  * it on `stream`, so it may start while that kernel is still running.  Before
  * it waits for that kernel to complete it reads ONLY context_lens and
@@ -330,9 +386,12 @@ PA_API int32_t pa_decode_max_splits(int32_t num_seqs, int32_t max_context_len, c
  *  ctas:         stream kernel: CTAs of its persistent grid.  The work is the concatenation,
  *                over groups of 8 kv heads and then sequences, of slabs of split_tokens
  *                tokens (an empty sequence counts one); CTA i of G = min(ctas, slabs S) takes
- *                slabs [i S / G, (i + 1) S / G).  0 for the split kernels.
+ *                slabs [i S / G, (i + 1) S / G).  4-bit pools: the same with teams of warps
+ *                for CTAs and groups of 8, 4, 2 or 1 kv heads, the largest that divides Hkv.
+ *                0 for the split kernels.
  *  split_tokens: split kernels: tokens per split (split k covers [k C, (k + 1) C)); stream
- *                kernel: tokens per slab (32 for E4M3 pools with head_dim 64, else 16).
+ *                kernel: tokens per slab (32 for E4M3 pools with head_dim 64, else 16); 4-bit
+ *                pools: tokens per slab.
  *  max_splits:   split kernels: splits per (sequence, kv head) at most; else 1.
  * Returns PA_OK, or the error the decode call itself would return for these arguments.
  */
@@ -510,6 +569,9 @@ PA_API int32_t pa_bm_num_cached_blocks(const pa_block_manager* bm);
  */
 PA_API int pa_copy_blocks(pa_bf16* k_cache, pa_bf16* v_cache, const int32_t* copies, int32_t n,
                           const pa_cache_desc* desc, void* stream);
+/* The same for 4-bit pools (see pa_append_kv_e2m1). */
+PA_API int pa_copy_blocks_e2m1(uint8_t* k_cache, uint8_t* v_cache, const int32_t* copies, int32_t n,
+                               const pa_cache_desc* desc, void* stream);
 
 #ifdef __cplusplus
 }

@@ -35,6 +35,7 @@ PA_FLAG_PDL = 2
 PA_FLAG_SELFTEST_STALL = 4
 PA_KV_BF16 = 0
 PA_KV_E4M3 = 1
+PA_KV_E2M1 = 2
 
 
 class PaError(RuntimeError):
@@ -139,6 +140,17 @@ lib.pa_prefill.restype = ctypes.c_int
 lib.pa_append_kv_e4m3.argtypes = [_vp, _vp, _vp, _i32, ctypes.c_float, ctypes.c_float, _vp, _vp, _DESC, _vp]
 lib.pa_append_kv_e4m3.restype = ctypes.c_int
 lib.pa_copy_blocks.restype = ctypes.c_int
+lib.pa_kv_cache_bytes.argtypes = [_DESC, _i32]
+lib.pa_kv_cache_bytes.restype = _sz
+lib.pa_append_kv_e2m1.argtypes = [_vp, _vp, _vp, _i32, ctypes.c_float, ctypes.c_float, _vp, _vp, _DESC, _vp]
+lib.pa_append_kv_e2m1.restype = ctypes.c_int
+lib.pa_rope_append_kv_e2m1.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i32, ctypes.c_float, ctypes.c_float,
+                                       ctypes.c_float, _vp, _vp, _DESC, _vp]
+lib.pa_rope_append_kv_e2m1.restype = ctypes.c_int
+lib.pa_gather_kv_e2m1.argtypes = [_vp, _vp, _vp, _i32, ctypes.c_float, ctypes.c_float, _vp, _vp, _DESC, _vp]
+lib.pa_gather_kv_e2m1.restype = ctypes.c_int
+lib.pa_copy_blocks_e2m1.argtypes = [_vp, _vp, _vp, _i32, _DESC, _vp]
+lib.pa_copy_blocks_e2m1.restype = ctypes.c_int
 lib.pa_pool_create.argtypes = [_i32, _vp, _i32, ctypes.POINTER(_vp)]
 lib.pa_pool_create.restype = ctypes.c_int
 lib.pa_pool_destroy.argtypes = [_vp]
@@ -189,14 +201,24 @@ def _dev(t, dtype_name: str, what: str):
 
 
 def _cache(t, desc: "CacheDesc", what: str, options=None):
-    """Device pointer of a KV cache tensor (bf16, or uint8 E4M3 codes when the options say so)
-    that holds at least the pool desc describes."""
+    """Device pointer of a KV cache tensor (bf16, or uint8 E4M3 codes or 4-bit pages when the
+    options say so) that holds at least the pool desc describes."""
+    kv_dtype = PA_KV_BF16 if options is None else options.kv_dtype
     if t is not None and not isinstance(t, int):
         need = int(desc.num_blocks) * desc.num_kv_heads * desc.block_size * desc.head_dim
+        if kv_dtype == PA_KV_E2M1:
+            need = need * 9 // 16
         if t.numel() < need:
             raise ValueError("%s holds %d elements, the pool described needs %d" % (what, t.numel(), need))
-    e4m3 = options is not None and options.kv_dtype == PA_KV_E4M3
-    return _dev(t, "uint8" if e4m3 else "bfloat16", what)
+    return _dev(t, "uint8" if kv_dtype in (PA_KV_E4M3, PA_KV_E2M1) else "bfloat16", what)
+
+
+def _rows(t, num_tokens: int, heads: int, desc: "CacheDesc", what: str):
+    """Device pointer of a bf16 tensor of at least num_tokens rows of `heads` heads."""
+    if t is not None and not isinstance(t, int) and t.numel() < num_tokens * heads * desc.head_dim:
+        raise ValueError("%s holds %d elements, %d tokens need %d" % (what, t.numel(), num_tokens,
+                                                                      num_tokens * heads * desc.head_dim))
+    return _dev(t, "bfloat16", what)
 
 
 def _stream(stream):
@@ -235,6 +257,61 @@ def pa_append_kv_e4m3(k, v, slot_mapping, k_scale: float, v_scale: float, k_cach
                                  float(v_scale), _cache(k_cache, desc, "k_cache", e4m3),
                                  _cache(v_cache, desc, "v_cache", e4m3), ctypes.byref(desc),
                                  _stream(stream)), "pa_append_kv_e4m3")
+
+
+_E2M1 = DecodeOptions(kv_dtype=PA_KV_E2M1)   # names the pools' type to _cache
+
+
+def pa_kv_cache_bytes(desc: CacheDesc, kv_dtype: int) -> int:
+    """Bytes of one cache tensor (K, or V) of this geometry and PA_KV_* type."""
+    n = int(lib.pa_kv_cache_bytes(ctypes.byref(desc), int(kv_dtype)))
+    if n == 0:
+        raise PaError(-1, "pa_kv_cache_bytes")
+    return n
+
+
+def pa_append_kv_e2m1(k, v, slot_mapping, k_scale: float, v_scale: float, k_cache, v_cache,
+                      desc: CacheDesc, stream=None, num_tokens: int | None = None) -> None:
+    """Quantizing append into 4-bit pools (uint8, pa_kv_cache_bytes(desc, PA_KV_E2M1) each)."""
+    n = int(slot_mapping.shape[0]) if num_tokens is None else int(num_tokens)
+    _check(lib.pa_append_kv_e2m1(_rows(k, n, desc.num_kv_heads, desc, "k"), _rows(v, n, desc.num_kv_heads, desc, "v"),
+                                 _dev(slot_mapping, "int64", "slot_mapping"), n, float(k_scale), float(v_scale),
+                                 _cache(k_cache, desc, "k_cache", _E2M1), _cache(v_cache, desc, "v_cache", _E2M1),
+                                 ctypes.byref(desc), _stream(stream)), "pa_append_kv_e2m1")
+
+
+def pa_rope_append_kv_e2m1(q, q_out, k, v, positions, slot_mapping, rope_theta: float, k_scale: float,
+                           v_scale: float, k_cache, v_cache, desc: CacheDesc, stream=None,
+                           num_tokens: int | None = None) -> None:
+    """RoPE of q (into q_out) and k, and the quantizing append into 4-bit pools, in one pass."""
+    n = int(slot_mapping.shape[0]) if num_tokens is None else int(num_tokens)
+    _check(lib.pa_rope_append_kv_e2m1(_rows(q, n, desc.num_q_heads, desc, "q"),
+                                      _rows(q_out, n, desc.num_q_heads, desc, "q_out"),
+                                      _rows(k, n, desc.num_kv_heads, desc, "k"),
+                                      _rows(v, n, desc.num_kv_heads, desc, "v"),
+                                      _dev(positions, "int32", "positions"),
+                                      _dev(slot_mapping, "int64", "slot_mapping"), n, float(rope_theta),
+                                      float(k_scale), float(v_scale), _cache(k_cache, desc, "k_cache", _E2M1),
+                                      _cache(v_cache, desc, "v_cache", _E2M1), ctypes.byref(desc),
+                                      _stream(stream)), "pa_rope_append_kv_e2m1")
+
+
+def pa_gather_kv_e2m1(k_cache, v_cache, slot_mapping, k_scale: float, v_scale: float, k, v, desc: CacheDesc,
+                      stream=None, num_tokens: int | None = None) -> None:
+    """The slots' rows of 4-bit pools read back as bf16 into k and v."""
+    n = int(slot_mapping.shape[0]) if num_tokens is None else int(num_tokens)
+    _check(lib.pa_gather_kv_e2m1(_cache(k_cache, desc, "k_cache", _E2M1), _cache(v_cache, desc, "v_cache", _E2M1),
+                                 _dev(slot_mapping, "int64", "slot_mapping"), n, float(k_scale), float(v_scale),
+                                 _rows(k, n, desc.num_kv_heads, desc, "k"), _rows(v, n, desc.num_kv_heads, desc, "v"),
+                                 ctypes.byref(desc), _stream(stream)), "pa_gather_kv_e2m1")
+
+
+def pa_copy_blocks_e2m1(k_cache, v_cache, copies, desc: CacheDesc, stream=None) -> None:
+    """pa_copy_blocks for 4-bit pools."""
+    n = int(copies.shape[0])
+    _check(lib.pa_copy_blocks_e2m1(_cache(k_cache, desc, "k_cache", _E2M1), _cache(v_cache, desc, "v_cache", _E2M1),
+                                   _dev(copies, "int32", "copies") if n else None, n, ctypes.byref(desc),
+                                   _stream(stream)), "pa_copy_blocks_e2m1")
 
 
 def pa_rope_append_kv(q, q_out, k, v, positions, slot_mapping, rope_theta: float, k_cache, v_cache,

@@ -9,6 +9,7 @@
 #include <atomic>
 
 #include "pa.h"
+#include "pa_e2m1.cuh"
 #include "pa_internal.h"
 
 namespace pa {
@@ -36,6 +37,17 @@ int check_desc(const pa_cache_desc* d) {
         return PA_ERR_UNSUPPORTED;  // row index of the pool must fit in 32 bits
     return PA_OK;
 }
+
+// 4-bit pools: the sizes they are built for.
+int check_e2m1_desc(const pa_cache_desc* d) {
+    const int rc = check_desc(d);
+    if (rc != PA_OK) return rc;
+    if ((d->head_dim != 64 && d->head_dim != 128) || !supported_block_size(d->block_size)) return PA_ERR_UNSUPPORTED;
+    return PA_OK;
+}
+
+// A scale of a quantized cache tensor: it and its reciprocal positive and finite.
+bool good_scale(float s) { return s > 0.f && s < INFINITY && 1.f / s < INFINITY; }
 
 // Optional override of the automatic split size, for tuning sweeps.
 int32_t env_split_tokens() {
@@ -102,13 +114,33 @@ int make_decode_plan(int32_t num_seqs, int32_t max_context_len, const pa_cache_d
     plan->split_tokens = 0;
     plan->max_splits = 1;
 
+    plan->slices = 0;
+    plan->desc_heads = 8;
     const bool fp8 = opt && opt->kv_dtype == PA_KV_E4M3;
+    if (opt && opt->kv_dtype == PA_KV_E2M1) {   // 4-bit pools: their own tensor kernel, any Hkv
+        if (kernel != PA_KERNEL_TENSOR) return PA_ERR_UNSUPPORTED;
+        plan->kernel = DecodeKernel::kE2m1;
+        plan->grid = e2m1_kernel_grid(d, opt->max_ctas);
+        if (plan->grid <= 0) return PA_ERR_CUDA;
+        plan->desc_heads = e2m1_head_group(d.num_kv_heads);
+        plan->slices = plan->grid * (8 / plan->desc_heads);
+        plan->off_lse = plan->off_desc + up((size_t)(d.num_kv_heads / plan->desc_heads) * num_seqs * 16);
+        const size_t rows = (size_t)plan->slices * 2 * d.num_kv_heads * G;
+        plan->off_o = plan->off_lse + up(rows * sizeof(float));
+        plan->bytes = plan->off_o + up(rows * (size_t)d.head_dim * sizeof(float));
+        if (opt->rope_theta > 0.f) {   // the rotated q of pa_append_decode
+            plan->off_qrot = plan->bytes;
+            plan->bytes += up((size_t)num_seqs * d.num_q_heads * d.head_dim * sizeof(uint16_t));
+        }
+        return PA_OK;
+    }
     if (fp8 && !(kernel == PA_KERNEL_TENSOR && stream_kernel_supports(d)))
         return PA_ERR_UNSUPPORTED;   // E4M3 pools: the whole-group tensor kernel only
     if (kernel == PA_KERNEL_TENSOR && stream_kernel_supports(d)) {
         plan->kernel = DecodeKernel::kStream;
         plan->grid = stream_kernel_grid(d, opt ? opt->max_ctas : 0, fp8);
         if (plan->grid <= 0) return PA_ERR_CUDA;
+        plan->slices = plan->grid;
         plan->off_lse = plan->off_desc + up((size_t)(d.num_kv_heads / 8) * num_seqs * 16);
         const size_t rows = (size_t)plan->grid * 2 * d.num_kv_heads * G;
         plan->off_o = plan->off_lse + up(rows * sizeof(float));
@@ -289,7 +321,81 @@ extern "C" int pa_copy_blocks(pa_bf16* k_cache, pa_bf16* v_cache, const int32_t*
     if (!k_cache || !v_cache || !copies || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
         !aligned(copies, 4))
         return PA_ERR_INVALID;
-    const cudaError_t e = launch_copy_blocks(k_cache, v_cache, copies, n, *desc, (cudaStream_t)stream);
+    const int64_t bytes = (int64_t)desc->num_kv_heads * desc->block_size * desc->head_dim * 2;
+    const cudaError_t e = launch_copy_blocks(k_cache, v_cache, copies, n, bytes, *desc, (cudaStream_t)stream);
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+extern "C" int pa_copy_blocks_e2m1(uint8_t* k_cache, uint8_t* v_cache, const int32_t* copies, int32_t n,
+                                   const pa_cache_desc* desc, void* stream) {
+    const int rc = check_e2m1_desc(desc);
+    if (rc != PA_OK) return rc;
+    if (n < 0) return PA_ERR_INVALID;
+    if (n == 0) return PA_OK;
+    if (!k_cache || !v_cache || !copies || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(copies, 4))
+        return PA_ERR_INVALID;
+    const int64_t bytes = (int64_t)desc->num_kv_heads * e2m1_page_bytes(desc->block_size, desc->head_dim);
+    const cudaError_t e = launch_copy_blocks(k_cache, v_cache, copies, n, bytes, *desc, (cudaStream_t)stream);
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+extern "C" size_t pa_kv_cache_bytes(const pa_cache_desc* desc, int32_t kv_dtype) {
+    if (check_desc(desc) != PA_OK) return 0;
+    const size_t rows = (size_t)desc->num_blocks * desc->num_kv_heads * desc->block_size;
+    if (kv_dtype == PA_KV_BF16) return rows * desc->head_dim * 2;
+    if (kv_dtype == PA_KV_E4M3) return rows * desc->head_dim;
+    if (kv_dtype != PA_KV_E2M1 || check_e2m1_desc(desc) != PA_OK) return 0;
+    return (size_t)desc->num_blocks * desc->num_kv_heads * e2m1_page_bytes(desc->block_size, desc->head_dim);
+}
+
+extern "C" int pa_append_kv_e2m1(const pa_bf16* k, const pa_bf16* v, const int64_t* slot_mapping,
+                                 int32_t num_tokens, float k_scale, float v_scale, uint8_t* k_cache,
+                                 uint8_t* v_cache, const pa_cache_desc* desc, void* stream) {
+    const int rc = check_e2m1_desc(desc);
+    if (rc != PA_OK) return rc;
+    if (num_tokens < 0 || !good_scale(k_scale) || !good_scale(v_scale)) return PA_ERR_INVALID;
+    if (num_tokens == 0) return PA_OK;
+    if (!k || !v || !slot_mapping || !k_cache || !v_cache || !aligned(k, 16) || !aligned(v, 16) ||
+        !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slot_mapping, 8))
+        return PA_ERR_INVALID;
+    const cudaError_t e = launch_append_e2m1(nullptr, nullptr, k, v, nullptr, slot_mapping, num_tokens, 0.f,
+                                             1.f / k_scale, 1.f / v_scale, k_cache, v_cache, *desc,
+                                             (cudaStream_t)stream);
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+extern "C" int pa_rope_append_kv_e2m1(const pa_bf16* q, pa_bf16* q_out, const pa_bf16* k, const pa_bf16* v,
+                                      const int32_t* positions, const int64_t* slot_mapping, int32_t num_tokens,
+                                      float rope_theta, float k_scale, float v_scale, uint8_t* k_cache,
+                                      uint8_t* v_cache, const pa_cache_desc* desc, void* stream) {
+    const int rc = check_e2m1_desc(desc);
+    if (rc != PA_OK) return rc;
+    if (num_tokens < 0 || !(rope_theta > 0.f) || !(rope_theta < INFINITY) || !good_scale(k_scale) ||
+        !good_scale(v_scale))
+        return PA_ERR_INVALID;
+    if (num_tokens == 0) return PA_OK;
+    if (!q || !q_out || !k || !v || !positions || !slot_mapping || !k_cache || !v_cache) return PA_ERR_INVALID;
+    if (!aligned(q, 16) || !aligned(q_out, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) ||
+        !aligned(v_cache, 16) || !aligned(slot_mapping, 8) || !aligned(positions, 4))
+        return PA_ERR_INVALID;
+    const cudaError_t e = launch_append_e2m1(q, q_out, k, v, positions, slot_mapping, num_tokens, rope_theta,
+                                             1.f / k_scale, 1.f / v_scale, k_cache, v_cache, *desc,
+                                             (cudaStream_t)stream);
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+extern "C" int pa_gather_kv_e2m1(const uint8_t* k_cache, const uint8_t* v_cache, const int64_t* slot_mapping,
+                                 int32_t num_tokens, float k_scale, float v_scale, pa_bf16* k, pa_bf16* v,
+                                 const pa_cache_desc* desc, void* stream) {
+    const int rc = check_e2m1_desc(desc);
+    if (rc != PA_OK) return rc;
+    if (num_tokens < 0 || !good_scale(k_scale) || !good_scale(v_scale)) return PA_ERR_INVALID;
+    if (num_tokens == 0) return PA_OK;
+    if (!k || !v || !slot_mapping || !k_cache || !v_cache || !aligned(k, 16) || !aligned(v, 16) ||
+        !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slot_mapping, 8))
+        return PA_ERR_INVALID;
+    const cudaError_t e = launch_gather_e2m1(k_cache, v_cache, slot_mapping, num_tokens, k_scale, v_scale, k, v,
+                                             *desc, (cudaStream_t)stream);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -335,13 +441,14 @@ extern "C" int pa_decode_describe(int32_t num_seqs, int32_t max_context_len, con
     DecodePlan plan;
     rc = make_decode_plan(num_seqs, max_context_len, *desc, options, &plan);
     if (rc != PA_OK) return rc;
-    out->kernel = plan.kernel == DecodeKernel::kStream  ? PA_KERNEL_TENSOR
+    out->kernel = plan.kernel == DecodeKernel::kStream || plan.kernel == DecodeKernel::kE2m1 ? PA_KERNEL_TENSOR
                   : plan.kernel == DecodeKernel::kSplit ? PA_KERNEL_TENSOR_SPLIT
                                                         : PA_KERNEL_SIMT;
-    out->ctas = plan.kernel == DecodeKernel::kStream ? plan.grid : 0;
+    out->ctas = plan.slices;
     out->split_tokens = plan.kernel == DecodeKernel::kStream
                             ? stream_slab_tokens(options && options->kv_dtype == PA_KV_E4M3, desc->head_dim)
-                            : plan.split_tokens;
+                        : plan.kernel == DecodeKernel::kE2m1 ? e2m1_slab_tokens(desc->head_dim)
+                                                             : plan.split_tokens;
     out->max_splits = plan.max_splits;
     return PA_OK;
 }
@@ -357,10 +464,13 @@ static int decode_call(const pa_bf16* q, const pa_bf16* k_new, const pa_bf16* v_
     if (options && (options->max_ctas < 0 || options->kernel < 0 || options->kernel > 3 ||
                     (options->flags & ~(PA_FLAG_CHECK | PA_FLAG_PDL | PA_FLAG_SELFTEST_STALL)) != 0 ||
                     !(options->rope_theta >= 0.f) || !(options->rope_theta < INFINITY) ||
-                    (options->kv_dtype != PA_KV_BF16 && options->kv_dtype != PA_KV_E4M3)))
+                    (options->kv_dtype != PA_KV_BF16 && options->kv_dtype != PA_KV_E4M3 &&
+                     options->kv_dtype != PA_KV_E2M1)))
         return PA_ERR_INVALID;
     const float rope_theta = options ? options->rope_theta : 0.f;
-    const bool fp8 = options && options->kv_dtype == PA_KV_E4M3;
+    const bool e2m1 = options && options->kv_dtype == PA_KV_E2M1;
+    const bool fp8 = options && options->kv_dtype == PA_KV_E4M3, scaled = fp8 || e2m1;
+    if (e2m1 && (!good_scale(options->k_scale) || !good_scale(options->v_scale))) return PA_ERR_INVALID;
     if (fp8 && (!(options->k_scale > 0.f) || !(options->k_scale < INFINITY) ||
                 !(options->v_scale > 0.f) || !(options->v_scale < INFINITY)))
         return PA_ERR_INVALID;
@@ -380,7 +490,8 @@ static int decode_call(const pa_bf16* q, const pa_bf16* k_new, const pa_bf16* v_
         return PA_ERR_WORKSPACE;
     char* ws = static_cast<char*>(workspace);
     DecodeParams p;
-    p.grid = plan.grid;
+    p.grid = plan.slices;
+    p.desc_heads = plan.desc_heads;
     p.selftest_stall = stall ? 1 : 0;
     p.wait_ns = stall ? kSelftestWaitNs : kDecodeWaitNs;
     p.q = q;
@@ -408,12 +519,13 @@ static int decode_call(const pa_bf16* q, const pa_bf16* k_new, const pa_bf16* v_
     p.max_context_len = max_context_len;
     p.split_tokens = plan.split_tokens;
     p.max_splits = plan.max_splits;
-    p.scale_log2 = scale * (fp8 ? options->k_scale : 1.f) * 1.4426950408889634f;
+    p.scale_log2 = scale * (scaled ? options->k_scale : 1.f) * 1.4426950408889634f;
     p.kv_fp8 = fp8 ? 1 : 0;
-    p.k_inv_scale = fp8 ? 1.f / options->k_scale : 1.f;
-    p.v_inv_scale = fp8 ? 1.f / options->v_scale : 1.f;
-    p.out_scale = fp8 ? options->v_scale : 1.f;
-    p.early = plan.kernel == DecodeKernel::kStream && options && (options->flags & PA_FLAG_PDL) ? 1 : 0;
+    p.k_inv_scale = scaled ? 1.f / options->k_scale : 1.f;
+    p.v_inv_scale = scaled ? 1.f / options->v_scale : 1.f;
+    p.out_scale = scaled ? options->v_scale : 1.f;
+    const bool stream_like = plan.kernel == DecodeKernel::kStream || plan.kernel == DecodeKernel::kE2m1;
+    p.early = stream_like && options && (options->flags & PA_FLAG_PDL) ? 1 : 0;
     p.rope_theta = plan.kernel == DecodeKernel::kStream ? rope_theta : 0.f;
     cudaError_t e;
     const cudaStream_t st = (cudaStream_t)stream;
@@ -421,11 +533,11 @@ static int decode_call(const pa_bf16* q, const pa_bf16* k_new, const pa_bf16* v_
         if (rope_theta > 0.f) {
             uint16_t* q_rot = reinterpret_cast<uint16_t*>(ws + plan.off_qrot);
             p.rope_theta = rope_theta;
-            e = launch_rope_append_at_end(p, q_rot, st);
+            e = e2m1 ? launch_append_e2m1_at_end(p, q_rot, st) : launch_rope_append_at_end(p, q_rot, st);
             p.rope_theta = 0.f;
             p.q = q_rot;
         } else {
-            e = launch_append_at_end(p, st);
+            e = e2m1 ? launch_append_e2m1_at_end(p, nullptr, st) : launch_append_at_end(p, st);
         }
         if (e != cudaSuccess) return PA_ERR_CUDA;
         p.k_new = p.v_new = nullptr;
@@ -434,12 +546,13 @@ static int decode_call(const pa_bf16* q, const pa_bf16* k_new, const pa_bf16* v_
         case DecodeKernel::kStream:
             e = launch_decode_stream(p, plan.grid, p.early != 0, st);
             break;
+        case DecodeKernel::kE2m1: e = launch_decode_e2m1(p, plan.grid, p.early != 0, st); break;
         case DecodeKernel::kSplit: e = launch_decode_tensor(p, st); break;
         default: e = launch_decode_simt(p, st); break;
     }
     // second pass: merge the pieces of every sequence that was cut
-    if (e == cudaSuccess && (plan.kernel == DecodeKernel::kStream || plan.max_splits > 1))
-        e = launch_merge(p, plan.kernel == DecodeKernel::kStream,
+    if (e == cudaSuccess && (stream_like || plan.max_splits > 1))
+        e = launch_merge(p, stream_like,
                          plan.kernel != DecodeKernel::kSimt, st);
     if (e != cudaSuccess) return PA_ERR_CUDA;
     if (options && (options->flags & PA_FLAG_CHECK))

@@ -140,9 +140,9 @@ cudaError_t launch_append_e4m3(const pa_bf16* k, const pa_bf16* v, const int64_t
     return cudaGetLastError();
 }
 
-cudaError_t launch_copy_blocks(pa_bf16* k_cache, pa_bf16* v_cache, const int32_t* copies, int32_t n,
-                               const pa_cache_desc& d, cudaStream_t stream) {
-    const int64_t cpb = (int64_t)d.num_kv_heads * d.block_size * d.head_dim / 8;
+cudaError_t launch_copy_blocks(void* k_cache, void* v_cache, const int32_t* copies, int32_t n,
+                               int64_t block_bytes, const pa_cache_desc& d, cudaStream_t stream) {
+    const int64_t cpb = block_bytes / 16;
     const int64_t total = (int64_t)n * cpb;
     if (total == 0) return cudaSuccess;
     int64_t blocks = (total + 255) / 256;

@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(PG * D / 4) merge_kernel(const DecodeParams p)
     int32_t nsplit;
     size_t first_row, row0, row_step;   // piece 0: first_row; piece k >= 1: row0 + (k-1) * row_step
     if (kStream) {
-        const int4 dsc = reinterpret_cast<const int4*>(p.seq_desc)[(size_t)(kvh / 8) * p.num_seqs + b];
+        const int4 dsc = reinterpret_cast<const int4*>(p.seq_desc)[(size_t)(kvh / p.desc_heads) * p.num_seqs + b];
         nsplit = dsc.x;
         if (nsplit <= 1) return;
         // a descriptor this launch's decode did not write (it gave up on a timed-out wait)
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(1024) merge_stream_kernel(const DecodeParams p
     wait_prerequisite();
     extern __shared__ float4 s_dyn[];
     const int32_t b = blockIdx.x, kvh = blockIdx.y, G = p.group, Hkv = p.num_kv_heads;
-    const int4 dsc = reinterpret_cast<const int4*>(p.seq_desc)[(size_t)(kvh / 8) * p.num_seqs + b];
+    const int4 dsc = reinterpret_cast<const int4*>(p.seq_desc)[(size_t)(kvh / p.desc_heads) * p.num_seqs + b];
     const int32_t nsplit = dsc.x;
     if (nsplit <= 1) return;
     // a descriptor this launch's decode did not write (it gave up on a timed-out wait) may be

@@ -50,7 +50,8 @@ struct DecodeParams {
     int32_t kv_fp8;                // caches hold E4M3 codes (uint8), values = code * scale
     float k_inv_scale, v_inv_scale;  // E4M3: float(1/scale) applied when quantizing new rows
     float out_scale;               // multiplies the normalised output (E4M3: the V scale; else 1)
-    int32_t grid;                  // stream kernel: CTAs of the launch (bounds the merge's reads)
+    int32_t grid;                  // stream kernels: slices of the launch (bounds the merge's reads)
+    int32_t desc_heads;            // stream kernels: kv heads that share one seq_desc row
 
     int32_t selftest_stall;        // PA_FLAG_SELFTEST_STALL: CTA 0 of the stream kernel idles
     unsigned long long wait_ns;    // limit of every bounded wait in the stream kernel
@@ -61,13 +62,16 @@ enum class DecodeKernel : int32_t {
     kSimt = 0,     // CUDA cores, one CTA per (sequence, kv head, split)
     kSplit = 1,    // tensor cores, persistent CTAs over (sequence, kv head, split) items
     kStream = 2,   // tensor cores, 8 kv heads per CTA, stream-partitioned slabs
+    kE2m1 = 3,     // tensor cores over 4-bit pools, slabs partitioned over teams of warps
 };
 
 struct DecodePlan {
     DecodeKernel kernel;
     int32_t split_tokens;          // kSimt / kSplit: tokens per split
     int32_t max_splits;            // kSimt / kSplit: splits per (sequence, kv head) at most
-    int32_t grid;                  // kStream: persistent CTAs (partial slots: 2 per CTA)
+    int32_t grid;                  // kStream, kE2m1: persistent CTAs
+    int32_t slices;                // kStream, kE2m1: equal slices of the work (2 partial slots each)
+    int32_t desc_heads;            // kStream, kE2m1: kv heads per group of the partition
     size_t off_desc, off_lse, off_o, off_qrot, bytes;
 };
 
@@ -111,8 +115,24 @@ cudaError_t launch_append_at_end(const DecodeParams& p, cudaStream_t stream);
 cudaError_t launch_append_e4m3(const pa_bf16* k, const pa_bf16* v, const int64_t* slots, int32_t T,
                                float k_inv_scale, float v_inv_scale, uint8_t* k_cache,
                                uint8_t* v_cache, const pa_cache_desc& d, cudaStream_t stream);
-cudaError_t launch_copy_blocks(pa_bf16* k_cache, pa_bf16* v_cache, const int32_t* copies, int32_t n,
-                               const pa_cache_desc& d, cudaStream_t stream);
+// block_bytes: bytes of a block in each cache (all its pages), a multiple of 16.
+cudaError_t launch_copy_blocks(void* k_cache, void* v_cache, const int32_t* copies, int32_t n,
+                               int64_t block_bytes, const pa_cache_desc& d, cudaStream_t stream);
+// 4-bit pools (format: pa_e2m1.cuh).  theta > 0: q (into q_out) and K turned by RoPE first.
+cudaError_t launch_append_e2m1(const pa_bf16* q, pa_bf16* q_out, const pa_bf16* k, const pa_bf16* v,
+                               const int32_t* positions, const int64_t* slots, int32_t T, float theta, float k_inv,
+                               float v_inv, uint8_t* k_cache, uint8_t* v_cache, const pa_cache_desc& d,
+                               cudaStream_t stream);
+// The newest token of each sequence, at position L-1 through the table; p.rope_theta > 0: K turned,
+// and q turned into q_out.
+cudaError_t launch_append_e2m1_at_end(const DecodeParams& p, uint16_t* q_out, cudaStream_t stream);
+cudaError_t launch_gather_e2m1(const uint8_t* k_cache, const uint8_t* v_cache, const int64_t* slots, int32_t T,
+                               float k_scale, float v_scale, pa_bf16* k, pa_bf16* v, const pa_cache_desc& d,
+                               cudaStream_t stream);
+cudaError_t launch_decode_e2m1(const DecodeParams& p, int grid, bool pdl, cudaStream_t stream);
+int e2m1_head_group(int num_kv_heads);
+int e2m1_slab_tokens(int head_dim);
+int e2m1_kernel_grid(const pa_cache_desc& d, int max_ctas);
 // RoPE + append through the slot mapping (pa_rope_append_kv).
 cudaError_t launch_rope_append(const pa_bf16* q, pa_bf16* q_out, const pa_bf16* k, const pa_bf16* v,
                                const int32_t* positions, const int64_t* slots, int32_t T, float theta,
