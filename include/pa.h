@@ -366,6 +366,33 @@ PA_API int pa_prefill(const pa_bf16* q, const pa_bf16* k_cache, const pa_bf16* v
                       const pa_cache_desc* desc, int32_t kernel, void* stream);
 
 /*
+ * Cross attention over a paged cache: the decoder side of an encoder-decoder model attends
+ * to its encoder's states.  (The pages have no counterpart; the formula is the attention
+ * above without the causal mask.)  The states' K and V of sequence b (encoder_lens[b] tokens,
+ * any number, zero included) sit in the paged pool as pa_append_kv put them; its query rows
+ * cu_seqlens_q[b] .. cu_seqlens_q[b+1] - 1 of q ([total_q][Hq][D] bf16), of any number, each
+ * attend to all of them:
+ *   out[row][h] = bf16( sum_j softmax_j(scale * q[row][h] . K_j) V_j ),
+ * K_j, V_j of kv head h / (Hq/Hkv).  A sequence without encoder tokens outputs zero rows.
+ * cu_seqlens_q as for pa_prefill; NULL (with max_q_len == 1): one query row a sequence, the
+ * decoding step, which runs the decode kernels (shapes as for pa_decode) and is the form to use
+ * there.  max_q_len >= every row count; max_encoder_len >= every encoder length (used by the
+ * NULL form only).  workspace: pa_cross_attention_workspace_size bytes, 256-byte aligned,
+ * zero-filled before its first use, one per call in flight; its status word as for pa_decode
+ * (more rows than max_q_len, or a length below zero or past the table: that sequence's rows are
+ * left unwritten, or for the NULL form the length clipped, and pa_decode_status reports it).
+ * head_dim 64 or 128; block sizes 8, 16, 32, 64 or multiples of 64.
+ * Errors: PA_ERR_INVALID, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE, PA_ERR_CUDA.
+ */
+PA_API size_t pa_cross_attention_workspace_size(int32_t num_seqs, int32_t max_q_len, int32_t max_encoder_len,
+                                                const pa_cache_desc* desc);
+PA_API int pa_cross_attention(const pa_bf16* q, const pa_bf16* k_cache, const pa_bf16* v_cache,
+                              const int32_t* block_tables, const int32_t* cu_seqlens_q,
+                              const int32_t* encoder_lens, int32_t num_seqs, int32_t max_q_len,
+                              int32_t max_encoder_len, float scale, pa_bf16* out, void* workspace,
+                              size_t workspace_bytes, const pa_cache_desc* desc, void* stream);
+
+/*
  * Synchronises `stream`, reads and clears the workspace's device status word.
  * Returns PA_OK, PA_ERR_BAD_BLOCK, PA_ERR_BAD_LENGTH, PA_ERR_TIMEOUT or
  * PA_ERR_UNSUPPORTED (a tensor-core kernel found its shared memory off the

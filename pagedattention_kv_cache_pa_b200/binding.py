@@ -140,6 +140,11 @@ lib.pa_prefill.restype = ctypes.c_int
 lib.pa_append_kv_e4m3.argtypes = [_vp, _vp, _vp, _i32, ctypes.c_float, ctypes.c_float, _vp, _vp, _DESC, _vp]
 lib.pa_append_kv_e4m3.restype = ctypes.c_int
 lib.pa_copy_blocks.restype = ctypes.c_int
+lib.pa_cross_attention_workspace_size.argtypes = [_i32, _i32, _i32, _DESC]
+lib.pa_cross_attention_workspace_size.restype = _sz
+lib.pa_cross_attention.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, ctypes.c_float, _vp, _vp, _sz,
+                                   _DESC, _vp]
+lib.pa_cross_attention.restype = ctypes.c_int
 lib.pa_kv_cache_bytes.argtypes = [_DESC, _i32]
 lib.pa_kv_cache_bytes.restype = _sz
 lib.pa_append_kv_e2m1.argtypes = [_vp, _vp, _vp, _i32, ctypes.c_float, ctypes.c_float, _vp, _vp, _DESC, _vp]
@@ -353,6 +358,29 @@ def pa_prefill(q, k_cache, v_cache, block_tables, cu_seqlens_q, context_lens, ma
                           n, int(max_q_len), float(scale), _dev(out, "bfloat16", "out"),
                           _dev(workspace, "uint8", "workspace"), int(workspace.numel()), ctypes.byref(desc),
                           _PREFILL_KERNELS[kernel], _stream(stream)), "pa_prefill")
+
+
+def pa_cross_attention_workspace_size(num_seqs: int, max_q_len: int, max_encoder_len: int, desc: CacheDesc) -> int:
+    n = int(lib.pa_cross_attention_workspace_size(int(num_seqs), int(max_q_len), int(max_encoder_len),
+                                                  ctypes.byref(desc)))
+    if n == 0:
+        raise PaError(-1, "pa_cross_attention_workspace_size")
+    return n
+
+
+def pa_cross_attention(q, k_cache, v_cache, block_tables, cu_seqlens_q, encoder_lens, max_q_len: int,
+                       max_encoder_len: int, scale: float, out, workspace, desc: CacheDesc, stream=None) -> None:
+    """Attention of each sequence's query rows to all of its encoder's tokens in the paged pool.
+
+    cu_seqlens_q: int32 [num_seqs + 1] row offsets, or None for one row a sequence (max_q_len 1)."""
+    n = int(encoder_lens.shape[0])
+    _check(lib.pa_cross_attention(_dev(q, "bfloat16", "q"), _cache(k_cache, desc, "k_cache"),
+                                  _cache(v_cache, desc, "v_cache"), _dev(block_tables, "int32", "block_tables"),
+                                  _dev(cu_seqlens_q, "int32", "cu_seqlens_q"),
+                                  _dev(encoder_lens, "int32", "encoder_lens"), n, int(max_q_len),
+                                  int(max_encoder_len), float(scale), _dev(out, "bfloat16", "out"),
+                                  _dev(workspace, "uint8", "workspace"), int(workspace.numel()),
+                                  ctypes.byref(desc), _stream(stream)), "pa_cross_attention")
 
 
 def pa_decode_workspace_size(num_seqs: int, max_context_len: int, desc: CacheDesc,

@@ -258,6 +258,32 @@ extern "C" int pa_append_kv_e4m3(const pa_bf16* k, const pa_bf16* v, const int64
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
+static PrefillParams prefill_params(const void* q, const void* k_cache, const void* v_cache,
+                                    const int32_t* block_tables, const int32_t* cu_seqlens_q,
+                                    const int32_t* lens, int32_t num_seqs, int32_t max_q_len, float scale,
+                                    pa_bf16* out, void* workspace, const pa_cache_desc& d) {
+    PrefillParams p;
+    p.q = static_cast<const uint16_t*>(q);
+    p.k_cache = static_cast<const uint16_t*>(k_cache);
+    p.v_cache = static_cast<const uint16_t*>(v_cache);
+    p.block_tables = block_tables;
+    p.cu_q = cu_seqlens_q;
+    p.context_lens = lens;
+    p.out = out;
+    p.status = static_cast<int32_t*>(workspace);
+    p.num_seqs = num_seqs;
+    p.num_blocks = d.num_blocks;
+    p.block_size = d.block_size;
+    p.num_kv_heads = d.num_kv_heads;
+    p.num_q_heads = d.num_q_heads;
+    p.head_dim = d.head_dim;
+    p.group = d.num_q_heads / d.num_kv_heads;
+    p.max_blocks_per_seq = d.max_blocks_per_seq;
+    p.max_q_len = max_q_len;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    return p;
+}
+
 extern "C" int pa_prefill(const pa_bf16* q, const pa_bf16* k_cache, const pa_bf16* v_cache,
                           const int32_t* block_tables, const int32_t* cu_seqlens_q,
                           const int32_t* context_lens, int32_t num_seqs, int32_t max_q_len, float scale,
@@ -283,25 +309,8 @@ extern "C" int pa_prefill(const pa_bf16* q, const pa_bf16* k_cache, const pa_bf1
         return PA_ERR_INVALID;
     if (!workspace || !aligned(workspace, kWorkspaceAlign) || workspace_bytes < kWorkspaceAlign)
         return PA_ERR_WORKSPACE;
-    PrefillParams p;
-    p.q = q;
-    p.k_cache = k_cache;
-    p.v_cache = v_cache;
-    p.block_tables = block_tables;
-    p.cu_q = cu_seqlens_q;
-    p.context_lens = context_lens;
-    p.out = out;
-    p.status = static_cast<int32_t*>(workspace);
-    p.num_seqs = num_seqs;
-    p.num_blocks = desc->num_blocks;
-    p.block_size = desc->block_size;
-    p.num_kv_heads = desc->num_kv_heads;
-    p.num_q_heads = desc->num_q_heads;
-    p.head_dim = desc->head_dim;
-    p.group = desc->num_q_heads / desc->num_kv_heads;
-    p.max_blocks_per_seq = desc->max_blocks_per_seq;
-    p.max_q_len = max_q_len;
-    p.scale_log2 = scale * 1.4426950408889634f;
+    const PrefillParams p = prefill_params(q, k_cache, v_cache, block_tables, cu_seqlens_q, context_lens, num_seqs,
+                                           max_q_len, scale, out, workspace, *desc);
     const cudaStream_t st = (cudaStream_t)stream;
     // automatic: the warp-specialized kernel where its TMA boxes tile the block size
     if (kernel == PA_PREFILL_AUTO)
@@ -590,6 +599,45 @@ extern "C" int pa_decode(const pa_bf16* q, const pa_bf16* k_cache, const pa_bf16
     return pa_decode_ex(q, k_cache, v_cache, block_tables, context_lens, num_seqs,
                         max_context_len, scale, out, workspace, workspace_bytes, desc, nullptr,
                         stream);
+}
+
+extern "C" size_t pa_cross_attention_workspace_size(int32_t num_seqs, int32_t max_q_len, int32_t max_encoder_len,
+                                                    const pa_cache_desc* desc) {
+    if (check_desc(desc) != PA_OK || num_seqs < 0 || max_q_len < 0 || max_encoder_len < 0) return 0;
+    const size_t step = max_q_len == 1 ? pa_decode_workspace_size(num_seqs, max_encoder_len, desc) : 0;
+    return step > kWorkspaceAlign ? step : kWorkspaceAlign;
+}
+
+extern "C" int pa_cross_attention(const pa_bf16* q, const pa_bf16* k_cache, const pa_bf16* v_cache,
+                                  const int32_t* block_tables, const int32_t* cu_seqlens_q,
+                                  const int32_t* encoder_lens, int32_t num_seqs, int32_t max_q_len,
+                                  int32_t max_encoder_len, float scale, pa_bf16* out, void* workspace,
+                                  size_t workspace_bytes, const pa_cache_desc* desc, void* stream) {
+    if (!(scale > 0.f) || !(scale < INFINITY) || max_encoder_len < 0) return PA_ERR_INVALID;
+    if (!cu_seqlens_q) {   // one query row a sequence: a decode over the encoder's tokens
+        if (max_q_len != 1) return PA_ERR_INVALID;
+        return pa_decode_ex(q, k_cache, v_cache, block_tables, encoder_lens, num_seqs, max_encoder_len, scale, out,
+                            workspace, workspace_bytes, desc, nullptr, stream);
+    }
+    const int rc = check_desc(desc);
+    if (rc != PA_OK) return rc;
+    if (num_seqs < 0 || num_seqs > 65535 || max_q_len < 0) return PA_ERR_INVALID;
+    if ((desc->head_dim != 64 && desc->head_dim != 128) || !prefill_ws_supports(desc->block_size) ||
+        desc->num_kv_heads > 65535)
+        return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || max_q_len == 0) return PA_OK;
+    if ((int64_t)max_q_len * (desc->num_q_heads / desc->num_kv_heads) > (int64_t)64 * 65535)
+        return PA_ERR_UNSUPPORTED;
+    if (!q || !k_cache || !v_cache || !block_tables || !encoder_lens || !out) return PA_ERR_INVALID;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        !aligned(block_tables, 4) || !aligned(cu_seqlens_q, 4) || !aligned(encoder_lens, 4))
+        return PA_ERR_INVALID;
+    if (!workspace || !aligned(workspace, kWorkspaceAlign) || workspace_bytes < kWorkspaceAlign)
+        return PA_ERR_WORKSPACE;
+    const PrefillParams p = prefill_params(q, k_cache, v_cache, block_tables, cu_seqlens_q, encoder_lens, num_seqs,
+                                           max_q_len, scale, out, workspace, *desc);
+    const cudaError_t e = launch_cross_ws(p, max_q_len, (cudaStream_t)stream);
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 extern "C" int pa_decode_status(void* workspace, size_t workspace_bytes, void* stream) {

@@ -24,6 +24,8 @@
 //   warp 5     TMA: K and V tiles of 64 keys into a ring of stages, one box of 64 dims x
 //              min(Bs, 64) tokens per block and 64-dim atom, swizzled by the copy engine; a
 //              stage is refilled once the MMAs that read it have completed.
+// kCausal = false is cross attention: every query row attends to all L tokens of its sequence (an
+// encoder's states), whatever its row count; a sequence without tokens writes zero rows.
 //   Q: two buffers.  The softmax warps request the next item's Q rows (cp.async, zeros past
 //   the chunk) when an item starts and publish them when it ends.
 //   An item's first P V, which overwrites O, waits until the softmax warps have read the
@@ -150,7 +152,9 @@ struct WsItem {
 // tiles attend to the most keys, so every sequence's longest items come first), then the
 // sequence, then the kv head.  Returns 1 for an item to run, 0 for none (a chunk with fewer
 // row tiles, or no queries), -1 for a sequence whose lengths cannot hold its queries (fewer
-// tokens than queries, past the table, or more queries than max_q_len).
+// tokens than queries, past the table, or more queries than max_q_len), 2 (cross attention only)
+// for rows with no token to attend to.
+template <bool kCausal>
 __device__ __forceinline__ int ws_item(const PrefillParams& p, long long i, WsItem& it, bool& tile0) {
     const long long nsh = (long long)p.num_seqs * p.num_kv_heads;
     int t_rev, rem;
@@ -168,18 +172,24 @@ __device__ __forceinline__ int ws_item(const PrefillParams& p, long long i, WsIt
     it.Tq = p.cu_q[it.b + 1] - it.q0;
     it.L = p.context_lens[it.b];
     if (it.Tq <= 0) return 0;
-    if (it.L < it.Tq || it.L > p.max_blocks_per_seq * p.block_size || it.Tq > p.max_q_len) return -1;
+    if ((kCausal ? it.L < it.Tq : it.L < 0) || it.L > p.max_blocks_per_seq * p.block_size || it.Tq > p.max_q_len)
+        return -1;
     it.rows = it.Tq * p.group;
     const int tile = (it.rows + kWsRows - 1) / kWsRows - 1 - t_rev;
     if (tile < 0) return 0;
     it.r0 = tile * kWsRows;
+    if (!kCausal) {
+        it.ntiles = (it.L + kWsKeys - 1) / kWsKeys;
+        it.pos_first = it.L - 1;
+        return it.L > 0 ? 1 : 2;
+    }
     const int last_tok = min(it.rows - 1, it.r0 + kWsRows - 1) / p.group;
     it.ntiles = (it.L - it.Tq + last_tok + 1 + kWsKeys - 1) / kWsKeys;   // keys up to the last row's position
     it.pos_first = it.L - it.Tq + it.r0 / p.group;
     return 1;
 }
 
-template <int D>
+template <int D, bool kCausal>
 __global__ void __launch_bounds__(kWsThreads, WsCfg<D>::kMinBlocks)
     prefill_ws_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap) {
@@ -243,9 +253,9 @@ __global__ void __launch_bounds__(kWsThreads, WsCfg<D>::kMinBlocks)
         const int rb = Bs < kWsKeys ? Bs : kWsKeys, nslot = kWsKeys / rb;
         int g = 0;
         for (long long r = 0, i = ws_index(0); i < n_items && !failed; i = ws_index(++r)) {
-            const int st_item = ws_item(p, i, it, tile0);
+            const int st_item = ws_item<kCausal>(p, i, it, tile0);
             if (st_item < 0 && tile0 && lane == 0) raise_status(p.status, kStatusBadLength);
-            if (st_item <= 0) continue;
+            if (st_item != 1) continue;
             const int* table = p.block_tables + (size_t)it.b * p.max_blocks_per_seq;
             for (int t = 0; t < it.ntiles; ++t, ++g) {
                 const int st = g % ST;
@@ -325,7 +335,7 @@ __global__ void __launch_bounds__(kWsThreads, WsCfg<D>::kMinBlocks)
             int g = 0, k = 0;
             bool ok = true;
             for (long long r = 0, i = ws_index(0); i < n_items && ok; i = ws_index(++r)) {
-                if (ws_item(p, i, it, tile0) <= 0) continue;
+                if (ws_item<kCausal>(p, i, it, tile0) != 1) continue;
                 const int qb = k & 1, nt = it.ntiles;
                 const uint32_t qbuf = s_q + qb * C::kQBytes;
                 ok = mbar_wait(bar_qf + 8 * qb, (uint32_t)((k >> 1) & 1), p.status) && wait_k(g);
@@ -396,8 +406,17 @@ __global__ void __launch_bounds__(kWsThreads, WsCfg<D>::kMinBlocks)
             if (lane == 0) mbar_arrive(bar_qf + 8 * qb);
         };
         auto next_item = [&](long long& r, WsItem& w) {      // the CTA's next item with work
-            for (long long i = ws_index(++r); i < n_items; i = ws_index(++r))
-                if (ws_item(p, i, w, tile0) > 0) return true;
+            for (long long i = ws_index(++r); i < n_items; i = ws_index(++r)) {
+                const int st_item = ws_item<kCausal>(p, i, w, tile0);
+                if (st_item == 1) return true;
+                if (!kCausal && st_item == 2 && w.r0 + tid < w.rows) {   // nothing to attend to: a zero row
+                    const int R = w.r0 + tid, tok = R / G;
+                    uint4* o = reinterpret_cast<uint4*>(
+                        p.out + ((size_t)(w.q0 + tok) * Hq + (size_t)w.kvh * G + (R - tok * G)) * D);
+#pragma unroll
+                    for (int c = 0; c < kCh; ++c) o[c] = make_uint4(0, 0, 0, 0);
+                }
+            }
             return false;
         };
         long long r = -1;
@@ -412,7 +431,7 @@ __global__ void __launch_bounds__(kWsThreads, WsCfg<D>::kMinBlocks)
             const bool has_nx = next_item(r, nx);
             if (has_nx) load_q(nx, (k + 1) & 1);
             const int R = it.r0 + tid, L = it.L;
-            const int pos = R < it.rows ? L - it.Tq + R / G : L - 1;   // padded rows: computed, not written
+            const int pos = kCausal && R < it.rows ? L - it.Tq + R / G : L - 1;   // padded rows: computed, not written
             float m_run = -INFINITY, l_run = 0.f;
             for (int t = 0; t < it.ntiles; ++t) {
                 const int gg = g + t;
@@ -590,14 +609,14 @@ bool ws_pool_map(CUtensorMap* map, const void* base, const PrefillParams& p) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+template <int D, bool kCausal>
 cudaError_t launch_ws(const PrefillParams& p, int max_q_len, cudaStream_t stream) {
     constexpr size_t smem = WsCfg<D>::kSmem;
     static std::atomic<uint64_t> attr_set{0};               // one bit per device
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!(attr_set.load(std::memory_order_acquire) & (1ull << dev))) {
-        const cudaError_t e = cudaFuncSetAttribute(prefill_ws_kernel<D>,
+        const cudaError_t e = cudaFuncSetAttribute(prefill_ws_kernel<D, kCausal>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
         attr_set.fetch_or(1ull << dev, std::memory_order_acq_rel);
@@ -614,7 +633,7 @@ cudaError_t launch_ws(const PrefillParams& p, int max_q_len, cudaStream_t stream
     const long long items = (long long)p.num_seqs * p.num_kv_heads * tiles;
     const long long ctas = std::min<long long>(items, (long long)sms * WsCfg<D>::kMinBlocks);
     dim3 grid((unsigned)ctas);
-    prefill_ws_kernel<D><<<grid, kWsThreads, smem, stream>>>(p, km, vm);
+    prefill_ws_kernel<D, kCausal><<<grid, kWsThreads, smem, stream>>>(p, km, vm);
     return cudaGetLastError();
 }
 
@@ -626,8 +645,14 @@ bool prefill_ws_supports(int block_size) {
 }
 
 cudaError_t launch_prefill_ws(const PrefillParams& p, int max_q_len, cudaStream_t stream) {
-    if (p.head_dim == 64) return launch_ws<64>(p, max_q_len, stream);
-    if (p.head_dim == 128) return launch_ws<128>(p, max_q_len, stream);
+    if (p.head_dim == 64) return launch_ws<64, true>(p, max_q_len, stream);
+    if (p.head_dim == 128) return launch_ws<128, true>(p, max_q_len, stream);
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_cross_ws(const PrefillParams& p, int max_q_len, cudaStream_t stream) {
+    if (p.head_dim == 64) return launch_ws<64, false>(p, max_q_len, stream);
+    if (p.head_dim == 128) return launch_ws<128, false>(p, max_q_len, stream);
     return cudaErrorInvalidValue;
 }
 
