@@ -366,6 +366,30 @@ PA_API int pa_prefill(const pa_bf16* q, const pa_bf16* k_cache, const pa_bf16* v
                       const pa_cache_desc* desc, int32_t kernel, void* stream);
 
 /*
+ * pa_prefill over a cache of any built type.  options (NULL: all zero): kernel as for
+ * pa_prefill; kv_dtype PA_KV_BF16 or PA_KV_E2M1 (4-bit pools, see pa_append_kv_e2m1, with
+ * their scales; kernel PA_PREFILL_AUTO or PA_PREFILL_TCGEN05_WS, block sizes of 4-bit pools).
+ * 4-bit K is widened to bf16 and V to f16 exactly, P is rounded to f16.  max_context_len: an
+ * upper bound of every context_lens[b].  workspace: pa_prefill_workspace_size bytes,
+ * 256-byte aligned, zero-filled before its first use, one per call in flight.  The rest, and
+ * the errors, as for pa_prefill; also PA_ERR_UNSUPPORTED for PA_KV_E4M3.
+ */
+typedef struct pa_prefill_options {
+    int32_t kernel;      /* PA_PREFILL_*                                                      */
+    int32_t kv_dtype;    /* PA_KV_BF16 (default) or PA_KV_E2M1                                */
+    float k_scale;       /* PA_KV_E2M1: scale of the K cache tensor (> 0)                     */
+    float v_scale;       /* PA_KV_E2M1: scale of the V cache tensor (> 0)                     */
+} pa_prefill_options;
+
+PA_API size_t pa_prefill_workspace_size(int32_t num_seqs, int32_t max_q_len, int32_t max_context_len,
+                                        const pa_cache_desc* desc, const pa_prefill_options* options);
+PA_API int pa_prefill_ex(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                         const int32_t* cu_seqlens_q, const int32_t* context_lens, int32_t num_seqs,
+                         int32_t max_q_len, int32_t max_context_len, float scale, pa_bf16* out,
+                         void* workspace, size_t workspace_bytes, const pa_cache_desc* desc,
+                         const pa_prefill_options* options, void* stream);
+
+/*
  * Cross attention over a paged cache: the decoder side of an encoder-decoder model attends
  * to its encoder's states.  (The pages have no counterpart; the formula is the attention
  * above without the causal mask.)  The states' K and V of sequence b (encoder_lens[b] tokens,

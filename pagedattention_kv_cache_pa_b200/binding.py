@@ -62,6 +62,11 @@ class DecodeOptions(ctypes.Structure):
                 ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
 
 
+class PrefillOptions(ctypes.Structure):
+    _fields_ = [("kernel", ctypes.c_int32), ("kv_dtype", ctypes.c_int32), ("k_scale", ctypes.c_float),
+                ("v_scale", ctypes.c_float)]
+
+
 class DecodePlanInfo(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_int32), ("ctas", ctypes.c_int32),
                 ("split_tokens", ctypes.c_int32), ("max_splits", ctypes.c_int32)]
@@ -140,6 +145,12 @@ lib.pa_prefill.restype = ctypes.c_int
 lib.pa_append_kv_e4m3.argtypes = [_vp, _vp, _vp, _i32, ctypes.c_float, ctypes.c_float, _vp, _vp, _DESC, _vp]
 lib.pa_append_kv_e4m3.restype = ctypes.c_int
 lib.pa_copy_blocks.restype = ctypes.c_int
+_POPTS = ctypes.POINTER(PrefillOptions)
+lib.pa_prefill_workspace_size.argtypes = [_i32, _i32, _i32, _DESC, _POPTS]
+lib.pa_prefill_workspace_size.restype = _sz
+lib.pa_prefill_ex.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, ctypes.c_float, _vp, _vp, _sz, _DESC,
+                              _POPTS, _vp]
+lib.pa_prefill_ex.restype = ctypes.c_int
 lib.pa_cross_attention_workspace_size.argtypes = [_i32, _i32, _i32, _DESC]
 lib.pa_cross_attention_workspace_size.restype = _sz
 lib.pa_cross_attention.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, ctypes.c_float, _vp, _vp, _sz,
@@ -358,6 +369,28 @@ def pa_prefill(q, k_cache, v_cache, block_tables, cu_seqlens_q, context_lens, ma
                           n, int(max_q_len), float(scale), _dev(out, "bfloat16", "out"),
                           _dev(workspace, "uint8", "workspace"), int(workspace.numel()), ctypes.byref(desc),
                           _PREFILL_KERNELS[kernel], _stream(stream)), "pa_prefill")
+
+
+def pa_prefill_workspace_size(num_seqs: int, max_q_len: int, max_context_len: int, desc: CacheDesc,
+                              options: PrefillOptions | None = None) -> int:
+    n = int(lib.pa_prefill_workspace_size(int(num_seqs), int(max_q_len), int(max_context_len), ctypes.byref(desc),
+                                          ctypes.byref(options) if options is not None else None))
+    if n == 0:
+        raise PaError(-1, "pa_prefill_workspace_size")
+    return n
+
+
+def pa_prefill_ex(q, k_cache, v_cache, block_tables, cu_seqlens_q, context_lens, max_q_len: int, max_context_len: int,
+                  scale: float, out, workspace, desc: CacheDesc, options: PrefillOptions | None = None,
+                  stream=None) -> None:
+    """pa_prefill over a cache of the options' type (bf16, or 4-bit pools with their scales)."""
+    n = int(context_lens.shape[0])
+    _check(lib.pa_prefill_ex(_dev(q, "bfloat16", "q"), _cache(k_cache, desc, "k_cache", options),
+                             _cache(v_cache, desc, "v_cache", options), _dev(block_tables, "int32", "block_tables"),
+                             _dev(cu_seqlens_q, "int32", "cu_seqlens_q"), _dev(context_lens, "int32", "context_lens"),
+                             n, int(max_q_len), int(max_context_len), float(scale), _dev(out, "bfloat16", "out"),
+                             _dev(workspace, "uint8", "workspace"), int(workspace.numel()), ctypes.byref(desc),
+                             ctypes.byref(options) if options is not None else None, _stream(stream)), "pa_prefill_ex")
 
 
 def pa_cross_attention_workspace_size(num_seqs: int, max_q_len: int, max_encoder_len: int, desc: CacheDesc) -> int:

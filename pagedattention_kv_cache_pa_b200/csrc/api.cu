@@ -281,6 +281,7 @@ static PrefillParams prefill_params(const void* q, const void* k_cache, const vo
     p.max_blocks_per_seq = d.max_blocks_per_seq;
     p.max_q_len = max_q_len;
     p.scale_log2 = scale * 1.4426950408889634f;
+    p.out_scale = 1.f;
     return p;
 }
 
@@ -599,6 +600,62 @@ extern "C" int pa_decode(const pa_bf16* q, const pa_bf16* k_cache, const pa_bf16
     return pa_decode_ex(q, k_cache, v_cache, block_tables, context_lens, num_seqs,
                         max_context_len, scale, out, workspace, workspace_bytes, desc, nullptr,
                         stream);
+}
+
+static int check_prefill_options(const pa_prefill_options* o) {
+    if (!o) return PA_OK;
+    if (o->kernel < PA_PREFILL_AUTO || o->kernel > PA_PREFILL_TCGEN05_WS) return PA_ERR_INVALID;
+    if (o->kv_dtype == PA_KV_E4M3) return PA_ERR_UNSUPPORTED;
+    if (o->kv_dtype == PA_KV_E2M1) {
+        if (!good_scale(o->k_scale) || !good_scale(o->v_scale)) return PA_ERR_INVALID;
+        return o->kernel == PA_PREFILL_AUTO || o->kernel == PA_PREFILL_TCGEN05_WS ? PA_OK : PA_ERR_UNSUPPORTED;
+    }
+    return o->kv_dtype == PA_KV_BF16 ? PA_OK : PA_ERR_INVALID;
+}
+
+extern "C" size_t pa_prefill_workspace_size(int32_t num_seqs, int32_t max_q_len, int32_t max_context_len,
+                                            const pa_cache_desc* desc, const pa_prefill_options* options) {
+    if (check_desc(desc) != PA_OK || num_seqs < 0 || max_q_len < 0 || max_context_len < 0 ||
+        check_prefill_options(options) != PA_OK)
+        return 0;
+    return kWorkspaceAlign;
+}
+
+extern "C" int pa_prefill_ex(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                             const int32_t* cu_seqlens_q, const int32_t* context_lens, int32_t num_seqs,
+                             int32_t max_q_len, int32_t max_context_len, float scale, pa_bf16* out,
+                             void* workspace, size_t workspace_bytes, const pa_cache_desc* desc,
+                             const pa_prefill_options* options, void* stream) {
+    int rc = check_prefill_options(options);
+    if (rc != PA_OK) return rc;
+    if (max_context_len < 0) return PA_ERR_INVALID;
+    if (!options || options->kv_dtype == PA_KV_BF16)
+        return pa_prefill(static_cast<const pa_bf16*>(q), static_cast<const pa_bf16*>(k_cache),
+                          static_cast<const pa_bf16*>(v_cache), block_tables, cu_seqlens_q, context_lens, num_seqs,
+                          max_q_len, scale, out, workspace, workspace_bytes, desc,
+                          options ? options->kernel : PA_PREFILL_AUTO, stream);
+    rc = check_desc(desc);
+    if (rc != PA_OK) return rc;
+    if (num_seqs < 0 || num_seqs > 65535 || max_q_len < 0 || !(scale > 0.f) || !(scale < INFINITY))
+        return PA_ERR_INVALID;
+    rc = check_e2m1_desc(desc);
+    if (rc != PA_OK) return rc;
+    if (desc->num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || max_q_len == 0) return PA_OK;
+    if ((int64_t)max_q_len * (desc->num_q_heads / desc->num_kv_heads) > (int64_t)64 * 65535)
+        return PA_ERR_UNSUPPORTED;
+    if (!q || !k_cache || !v_cache || !block_tables || !cu_seqlens_q || !context_lens || !out)
+        return PA_ERR_INVALID;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        !aligned(block_tables, 4) || !aligned(cu_seqlens_q, 4) || !aligned(context_lens, 4))
+        return PA_ERR_INVALID;
+    if (!workspace || !aligned(workspace, kWorkspaceAlign) || workspace_bytes < kWorkspaceAlign)
+        return PA_ERR_WORKSPACE;
+    PrefillParams p = prefill_params(q, k_cache, v_cache, block_tables, cu_seqlens_q, context_lens, num_seqs,
+                                     max_q_len, scale * options->k_scale, out, workspace, *desc);
+    p.out_scale = options->v_scale;
+    const cudaError_t e = launch_prefill_e2m1(p, max_q_len, (cudaStream_t)stream);
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 extern "C" size_t pa_cross_attention_workspace_size(int32_t num_seqs, int32_t max_q_len, int32_t max_encoder_len,

@@ -90,6 +90,7 @@ struct PrefillParams {
     int32_t max_blocks_per_seq;
     int32_t max_q_len;             // the caller's bound on every sequence's query count
     float scale_log2;
+    float out_scale;               // multiplies the normalised output (4-bit pools: the V scale)
 };
 cudaError_t launch_prefill(const PrefillParams& p, int max_q_len, cudaStream_t stream);
 cudaError_t launch_prefill_tc(const PrefillParams& p, int max_q_len, cudaStream_t stream);
@@ -132,6 +133,8 @@ cudaError_t launch_gather_e2m1(const uint8_t* k_cache, const uint8_t* v_cache, c
                                float k_scale, float v_scale, pa_bf16* k, pa_bf16* v, const pa_cache_desc& d,
                                cudaStream_t stream);
 cudaError_t launch_decode_e2m1(const DecodeParams& p, int grid, bool pdl, cudaStream_t stream);
+// causal prefill over 4-bit pools
+cudaError_t launch_prefill_e2m1(const PrefillParams& p, int max_q_len, cudaStream_t stream);
 int e2m1_head_group(int num_kv_heads);
 int e2m1_slab_tokens(int head_dim);
 int e2m1_kernel_grid(const pa_cache_desc& d, int max_ctas);

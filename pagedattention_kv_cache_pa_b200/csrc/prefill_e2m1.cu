@@ -1,0 +1,645 @@
+// Paged (chunked) prefill attention over a 4-bit (E2M1) cache, on the fifth-generation tensor cores.
+//
+// The operation is pa_prefill's: sequence b's last Tq tokens attend causally to its L cached
+// tokens, whose K and V the cache holds in 4 bits (format: pa_e2m1.cuh).  The matrix products need
+// both operands in 16 bits, so a tile of keys has to be widened first; that costs about as many
+// instructions as half the softmax of 128 rows, so a CTA takes two tiles of 128 query rows
+// against each widened tile of 64 keys.
+//
+// Persistent CTAs, one per SM; items (256 query rows, kv head, sequence) are ordered by size and
+// taken in zigzag as in prefill_ws.cu.  Warps with one job each meet through mbarriers only:
+//   warps 0-3, 4-7  softmax of row tile 0 and 1: thread = row.  S out of tensor memory, causal mask,
+//                   running max with lazy rescale of O in tensor memory, P (f16) back to it.
+//   warps 8-11      widening: thread = half a key row.  Codes and scales of the next tile are in
+//                   flight in registers while this one is widened: V to f16 (one conversion and one
+//                   product a pair, exact), K to bf16 (q's type; the f16 pattern of a code shifted
+//                   into bf16's fields is the code times 2^-112, which the scale's factor undoes,
+//                   exact too).  Rows past the sequence are zero, so P = 0 never meets a NaN there.
+//   warp 12         (of a fourth warpgroup) MMA issue: S(t + 1) of each row tile as soon as its softmax has read S(t), then
+//                   O += P(t) V(t).
+// K and V tiles have rings of their own: a K stage is free after the two S products, long before
+// its V is.  Tensor memory: S 2 x 64 columns, P 2 x 32, O 2 x D.
+//
+// Every wait is bounded (2 s, then the timeout status bit); the tensor memory is freed and no
+// asynchronous operation is left when a CTA exits.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "pa_device.cuh"
+#include "pa_e2m1.cuh"
+#include "pa_internal.h"
+#include "pa_ptx.cuh"
+#include "pa_umma.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kRows = 128;                 // query rows per softmax group (tensor-memory lanes)
+constexpr int kItemRows = 2 * kRows;
+constexpr int kKeys = 64;
+constexpr int kWiden0 = 8, kMmaWarp = 12;  // first widening warp, the MMA warp
+constexpr int kThreads = 512;              // four warpgroups: softmax 0, softmax 1, widening, MMA
+// Registers a thread: 128 at launch, moved from the last two warpgroups to the softmax ones.  The
+// shares add up to the launch's: 2 x 176 + 104 + 56 = 4 x 128.
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 176, kWidenRegs = 104, kMmaRegs = 56;
+static_assert(2 * kSoftmaxRegs + kWidenRegs + kMmaRegs == 4 * kLaunchRegs, "register shares");
+constexpr float kRescaleLog2 = 8.f;
+
+template <int D>
+struct PCfg {
+    static constexpr int kStages = D == 64 ? 4 : 3;
+    static constexpr int kQBytes = kRows * D * 2;
+    static constexpr int kTileBytes = kKeys * D * 2;
+    static constexpr int kOffQ = 0;                                // [buffer][group]
+    static constexpr int kOffK = kOffQ + 4 * kQBytes;
+    static constexpr int kOffV = kOffK + kStages * kTileBytes;
+    static constexpr int kOffBar = kOffV + kStages * kTileBytes;
+    // s_full[2], s_free[2], p_full[2], o_done[2], o_free[2], q_full[2][2], drain, then per stage
+    // k_full, k_empty, v_full, v_empty
+    static constexpr int kBars = 15 + 4 * kStages;
+    static constexpr int kSmem = kOffBar + kBars * 8 + 16;
+    static constexpr int kColS = 0, kColP = 128, kColO = 192;      // S: 64 a group, P: 32, O: D
+    static constexpr uint32_t kTmemCols = 512;
+    static_assert(kColO + 2 * D <= 512 && kSmem <= 227 * 1024, "tensor and shared memory of one CTA");
+};
+
+template <int ROWS>
+__device__ __forceinline__ uint32_t sw128(int row, int c) {        // 16-byte chunk c of a row
+    return (uint32_t)((c >> 3) * (ROWS * 128) + row * 128 + ((((c & 7) ^ (row & 7))) << 4));
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void f2_split(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ void tmem_scale32(uint32_t taddr, float a) {
+    uint32_t r[32];
+    tmem_ld32(taddr, r);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * a);
+    tmem_st32(taddr, r);
+}
+
+// The item a CTA takes in its round r: rounds of grid items in order, CTAs in zigzag.
+__device__ __forceinline__ long long item_index(long long r) {
+    return r * gridDim.x + ((r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
+// One work item: up to 256 query rows of one kv head of one sequence.
+struct Item {
+    int b, kvh, q0, Tq, L, rows, r0;
+    int nt[2];                             // key tiles of either row tile (0: no rows)
+};
+
+// Item i, as in prefill_ws.cu: the last row tiles of every chunk first.  1: an item to run; 0: none;
+// -1: a sequence whose lengths cannot hold its queries.
+__device__ __forceinline__ int get_item(const PrefillParams& p, long long i, Item& it, bool& tile0) {
+    const long long nsh = (long long)p.num_seqs * p.num_kv_heads;
+    int t_rev, rem;
+    if (i <= 0x7fffffffLL && nsh <= 0x7fffffffLL) {
+        t_rev = (int)((unsigned)i / (unsigned)nsh);
+        rem = (int)((unsigned)i - (unsigned)t_rev * (unsigned)nsh);
+    } else {
+        t_rev = (int)(i / nsh);
+        rem = (int)(i - (long long)t_rev * nsh);
+    }
+    it.b = rem / p.num_kv_heads;
+    it.kvh = rem - it.b * p.num_kv_heads;
+    tile0 = t_rev == 0 && it.kvh == 0;
+    it.q0 = p.cu_q[it.b];
+    it.Tq = p.cu_q[it.b + 1] - it.q0;
+    it.L = p.context_lens[it.b];
+    if (it.Tq <= 0) return 0;
+    if (it.L < it.Tq || it.L > p.max_blocks_per_seq * p.block_size || it.Tq > p.max_q_len) return -1;
+    it.rows = it.Tq * p.group;
+    const int tile = (it.rows + kItemRows - 1) / kItemRows - 1 - t_rev;
+    if (tile < 0) return 0;
+    it.r0 = tile * kItemRows;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        const int first = it.r0 + g * kRows;
+        const int last_tok = min(it.rows - 1, first + kRows - 1) / p.group;
+        it.nt[g] = first < it.rows ? (it.L - it.Tq + last_tok + 1 + kKeys - 1) / kKeys : 0;
+    }
+    return 1;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) prefill_e2m1_kernel(const PrefillParams p) {
+    using C = PCfg<D>;
+    constexpr int kCh = D / 8, ST = C::kStages;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t s_base = smem_u32(smem);
+    const uint32_t s_q = s_base + C::kOffQ, s_k = s_base + C::kOffK, s_v = s_base + C::kOffV;
+    const uint32_t bars = s_base + C::kOffBar;
+    auto bar_s = [&](int g) { return bars + 8 * g; };
+    auto bar_sf = [&](int g) { return bars + 16 + 8 * g; };
+    auto bar_p = [&](int g) { return bars + 32 + 8 * g; };
+    auto bar_o = [&](int g) { return bars + 48 + 8 * g; };
+    auto bar_of = [&](int g) { return bars + 64 + 8 * g; };
+    auto bar_q = [&](int buf, int g) { return bars + 80 + 16 * buf + 8 * g; };
+    const uint32_t bar_drain = bars + 112;
+    const uint32_t bar_kf = bars + 120, bar_ke = bar_kf + 8 * ST, bar_vf = bar_ke + 8 * ST, bar_ve = bar_vf + 8 * ST;
+    const uint32_t s_tmem = bars + C::kBars * 8;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = p.group, Hq = p.num_q_heads, Hkv = p.num_kv_heads, Bs = p.block_size;
+    const long long n_items =
+        (long long)p.num_seqs * Hkv * ((p.max_q_len * (long long)G + kItemRows - 1) / kItemRows);
+
+    if (s_base & 1023u) {                                    // the swizzle needs 1024-byte-aligned tiles
+        if (tid == 0) raise_status(p.status, kStatusSmemAlign);
+        return;
+    }
+    if (warp == 0) {
+        tmem_alloc(s_tmem, C::kTmemCols);
+        tmem_relinquish();
+    }
+    if (tid == 0) {
+        for (int g = 0; g < 2; ++g) {
+            mbar_init(bar_s(g), 1);
+            mbar_init(bar_sf(g), 4);                         // one arrival per softmax warp of the group
+            mbar_init(bar_p(g), 4);
+            mbar_init(bar_o(g), 1);
+            mbar_init(bar_of(g), 4);
+            mbar_init(bar_q(0, g), 4);
+            mbar_init(bar_q(1, g), 4);
+        }
+        mbar_init(bar_drain, 1);
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(bar_kf + 8 * i, 4);                    // one arrival per widening warp
+            mbar_init(bar_vf + 8 * i, 4);
+            mbar_init(bar_ke + 8 * i, 1);
+            mbar_init(bar_ve + 8 * i, 1);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    uint32_t tmem;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(s_tmem) : "memory");
+    bool tile0;
+
+    if (warp >= kWiden0 && warp < kMmaWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWidenRegs));
+        // ============================== widening ==============================
+        // Thread = (key, half): 16-byte blocks of codes `half` (and half + 2 at D = 128) of the row.
+        constexpr int kBlk = D / 64;                         // 16-byte code blocks a thread
+        const int pt = tid - kWiden0 * 32, key = pt >> 1, half = pt & 1;
+        const size_t page_bytes = e2m1_page_bytes(Bs, D);
+        const int bs_shift = 31 - __clz(Bs);
+        const uint8_t* kc = reinterpret_cast<const uint8_t*>(p.k_cache);
+        const uint8_t* vc = reinterpret_cast<const uint8_t*>(p.v_cache);
+        struct Cur {                                         // a tile, and this thread's block of it
+            Item it;
+            int t, id;
+            bool has;
+        };
+        struct Raw {
+            uint4 k[kBlk], v[kBlk];
+            uint32_t ks[kBlk], vs[kBlk];                     // two scale bytes a block, one per half word
+        };
+        long long r = -1;
+        auto lookup = [&](Cur& c) {                          // the physical block of the thread's key
+            const int kp = c.t * kKeys + key;
+            c.id = -1;
+            if (c.has && kp < c.it.L) c.id = __ldg(p.block_tables + (size_t)c.it.b * p.max_blocks_per_seq + (kp >> bs_shift));
+        };
+        auto next = [&](const Cur& c, Cur& n) {
+            n = c;
+            if (c.has && ++n.t < max(c.it.nt[0], c.it.nt[1])) {
+                lookup(n);
+                return;
+            }
+            n.has = false;
+            for (long long i = item_index(++r); i < n_items; i = item_index(++r)) {
+                const int st = get_item(p, i, n.it, tile0);
+                if (st < 0 && tile0 && pt == 0) raise_status(p.status, kStatusBadLength);
+                if (st == 1) {
+                    n.has = true;
+                    n.t = 0;
+                    break;
+                }
+            }
+            lookup(n);
+        };
+        auto load = [&](const Cur& c, Raw& x) {
+            bool ok = c.has && c.t * kKeys + key < c.it.L;
+            if (ok && (c.id < 0 || c.id >= p.num_blocks)) {
+                raise_status(p.status, kStatusBadBlock);
+                ok = false;
+            }
+#pragma unroll
+            for (int i = 0; i < kBlk; ++i) {
+                x.k[i] = x.v[i] = make_uint4(0, 0, 0, 0);
+                x.ks[i] = x.vs[i] = 0u;
+            }
+            if (!ok) return;
+            const int off = (c.t * kKeys + key) & (Bs - 1);
+            const size_t page = ((size_t)c.id * Hkv + c.it.kvh) * page_bytes;
+            const size_t row = page + off * (D / 2), sc = page + Bs * (D / 2) + off;
+#pragma unroll
+            for (int i = 0; i < kBlk; ++i) {
+                const int blk = half + 2 * i;
+                x.k[i] = __ldg(reinterpret_cast<const uint4*>(kc + row + 16 * blk));
+                x.v[i] = __ldg(reinterpret_cast<const uint4*>(vc + row + 16 * blk));
+                x.ks[i] = (uint32_t)__ldg(kc + sc + (2 * blk) * Bs) | ((uint32_t)__ldg(kc + sc + (2 * blk + 1) * Bs) << 16);
+                x.vs[i] = (uint32_t)__ldg(vc + sc + (2 * blk) * Bs) | ((uint32_t)__ldg(vc + sc + (2 * blk + 1) * Bs) << 16);
+            }
+        };
+        int g = 0;                                           // tiles so far (ring counter)
+        auto put = [&](uint32_t dst, const uint32_t (&h)[4]) {
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                         : "memory");
+        };
+        auto publish = [&](uint32_t bar) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+        auto widen = [&](const Raw& x) -> bool {
+            const int st = g % ST;
+            if (g >= ST && !warp_wait(bar_ke + 8 * st, (uint32_t)((g / ST - 1) & 1), p.status)) return false;
+#pragma unroll
+            for (int i = 0; i < kBlk; ++i) {
+                const uint32_t w[4] = {x.k[i].x, x.k[i].y, x.k[i].z, x.k[i].w};
+#pragma unroll
+#pragma unroll
+                for (int gr = 0; gr < 2; ++gr) {             // one scale group: two words
+                    const float s = f16x2_to_f32x2(e4m3x2_to_f16x2((x.ks[i] >> (16 * gr)) & 0xFFu)).x;
+                    const uint32_t sb = pack_bf16x2(s * 0x1p112f, s * 0x1p112f);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        uint32_t h[4];
+                        e2m1x8_to_f16x2x4(w[2 * gr + u], h);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            h[j] = mul_bf16x2(((h[j] >> 3) & 0x0FFF0FFFu) | (h[j] & 0x80008000u), sb);
+                        put(s_k + st * C::kTileBytes + sw128<kKeys>(key, 4 * (half + 2 * i) + 2 * gr + u), h);
+                    }
+                }
+            }
+            publish(bar_kf + 8 * st);
+            if (g >= ST && !warp_wait(bar_ve + 8 * st, (uint32_t)((g / ST - 1) & 1), p.status)) return false;
+#pragma unroll
+            for (int i = 0; i < kBlk; ++i) {
+                const uint32_t w[4] = {x.v[i].x, x.v[i].y, x.v[i].z, x.v[i].w};
+#pragma unroll
+#pragma unroll
+                for (int gr = 0; gr < 2; ++gr) {
+                    const uint32_t b = (x.vs[i] >> (16 * gr)) & 0xFFu, s = e4m3x2_to_f16x2(b | (b << 8));
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        uint32_t h[4];
+                        e2m1x8_to_f16x2x4(w[2 * gr + u], h);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) h[j] = mul_f16x2(h[j], s);
+                        put(s_v + st * C::kTileBytes + sw128<kKeys>(key, 4 * (half + 2 * i) + 2 * gr + u), h);
+                    }
+                }
+            }
+            publish(bar_vf + 8 * st);
+            ++g;
+            return true;
+        };
+        Cur a, b;
+        Raw xa, xb;
+        a.has = false;
+        a.t = 0;
+        next(a, a);
+        load(a, xa);
+        next(a, b);
+        while (a.has) {                                      // a: loaded; b: its block is known
+            load(b, xb);
+            next(b, a);
+            if (!widen(xa)) break;
+            if (!b.has) break;
+            load(a, xa);
+            next(a, b);
+            if (!widen(xb)) break;
+        }
+    } else if (warp >= kMmaWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+        // ================================ MMA ================================
+        if (warp == kMmaWarp && lane == 0) {
+            constexpr uint32_t kIdescS = umma_idesc_bf16(kRows, kKeys, false);
+            constexpr uint32_t kIdescO = umma_idesc_f16(kRows, D, true);
+            int g = 0, tiles[2] = {0, 0}, items[2] = {0, 0};   // ring counter; tiles and items of either row tile
+            bool ok = true;
+            Item it;
+            auto issue_s = [&](int gr, int gg) {             // S of row tile gr = Q K^T
+                const uint32_t q = s_q + (2 * (items[gr] & 1) + gr) * C::kQBytes, kt = s_k + (gg % ST) * C::kTileBytes;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint64_t ad = umma_desc_sw128(q + (ks >> 2) * (kRows * 128) + (ks & 3) * 32, 16, 1024);
+                    const uint64_t bd = umma_desc_sw128(kt + (ks >> 2) * (kKeys * 128) + (ks & 3) * 32, 16, 1024);
+                    umma_bf16_ss(tmem + C::kColS + gr * 64, ad, bd, kIdescS, ks > 0);
+                }
+                umma_commit(bar_s(gr));
+            };
+            auto issue_o = [&](int gr, int gg, bool first) { // O of row tile gr (+)= P V
+                const uint32_t vt = s_v + (gg % ST) * C::kTileBytes;
+#pragma unroll
+                for (int kk = 0; kk < kKeys / 16; ++kk) {
+                    const uint64_t bd = umma_desc_sw128(vt + kk * 16 * 128, kKeys * 128, 1024);
+                    umma_bf16_ts(tmem + C::kColO + gr * D, tmem + C::kColP + gr * 32 + kk * 8, bd, kIdescO,
+                                 (!first || kk > 0) ? 1u : 0u);
+                }
+                umma_commit(bar_o(gr));
+            };
+            auto wait_k = [&](int gg) { return mbar_wait(bar_kf + 8 * (gg % ST), (uint32_t)((gg / ST) & 1), p.status); };
+            auto wait_v = [&](int gg) { return mbar_wait(bar_vf + 8 * (gg % ST), (uint32_t)((gg / ST) & 1), p.status); };
+            for (long long r = 0, i = item_index(0); i < n_items && ok; i = item_index(++r)) {
+                if (get_item(p, i, it, tile0) != 1) continue;
+                const int nt = max(it.nt[0], it.nt[1]);
+                if (!(ok = wait_k(g))) break;
+#pragma unroll
+                for (int gr = 0; gr < 2 && ok; ++gr) {
+                    if (!it.nt[gr]) continue;
+                    ok = mbar_wait(bar_q(items[gr] & 1, gr), (uint32_t)((items[gr] >> 1) & 1), p.status);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    issue_s(gr, g);
+                }
+                if (!ok) break;
+                umma_commit(bar_ke + 8 * (g % ST));
+                for (int t = 0; t < nt && ok; ++t) {
+                    const int gg = g + t;
+                    if (t + 1 < nt) {                        // the next scores, once these have been read
+                        if (!(ok = wait_k(gg + 1))) break;
+#pragma unroll
+                        for (int gr = 0; gr < 2 && ok; ++gr) {
+                            if (t + 1 >= it.nt[gr]) continue;
+                            ok = mbar_wait(bar_sf(gr), (uint32_t)((tiles[gr] + t) & 1), p.status);
+                            if (!ok) break;
+                            tc_fence_after_sync();
+                            issue_s(gr, gg + 1);
+                        }
+                        if (!ok) break;
+                        umma_commit(bar_ke + 8 * ((gg + 1) % ST));
+                    }
+                    if (!(ok = wait_v(gg))) break;
+#pragma unroll
+                    for (int gr = 0; gr < 2 && ok; ++gr) {
+                        if (t >= it.nt[gr]) continue;
+                        // an item's first product overwrites O: not before the last item's was read
+                        ok = mbar_wait(bar_p(gr), (uint32_t)((tiles[gr] + t) & 1), p.status) &&
+                             (t > 0 || items[gr] == 0 ||
+                              mbar_wait(bar_of(gr), (uint32_t)((items[gr] - 1) & 1), p.status));
+                        if (!ok) break;
+                        tc_fence_after_sync();
+                        issue_o(gr, gg, t == 0);
+                    }
+                    if (!ok) break;
+                    umma_commit(bar_ve + 8 * (gg % ST));
+                }
+                g += nt;
+#pragma unroll
+                for (int gr = 0; gr < 2; ++gr) {
+                    if (!it.nt[gr]) continue;
+                    // the last tile's scores were read too, with no S issued after it
+                    ok = ok && mbar_wait(bar_sf(gr), (uint32_t)((tiles[gr] + it.nt[gr] - 1) & 1), p.status);
+                    tiles[gr] += it.nt[gr];
+                    ++items[gr];
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        // ============================== softmax ==============================
+        const int gr = warp >> 2, tr = tid & (kRows - 1);    // row tile, row in it
+        const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const float sl2 = p.scale_log2;
+        auto wait_o = [&](int tt) { return warp_wait(bar_o(gr), (uint32_t)(tt & 1), p.status); };
+        constexpr int kRowStep = kRows / kCh;
+        auto load_q = [&](const Item& w, int buf) {
+            const uint32_t qbuf = s_q + (2 * buf + gr) * C::kQBytes;
+            const int tok_step = kRowStep / G, g_step = kRowStep - tok_step * G;
+            const int ch = tr % kCh;
+            int row = tr / kCh, R = w.r0 + gr * kRows + row, tok = R / G, gq = R - tok * G;
+#pragma unroll 4
+            for (int j = 0; j < kRows / kRowStep; ++j) {
+                const bool live = R < w.rows;
+                const uint16_t* src =
+                    p.q + (((size_t)(w.q0 + (live ? tok : 0)) * Hq + (size_t)w.kvh * G + (live ? gq : 0)) * D + ch * 8);
+                cp_async16(qbuf + sw128<kRows>(row, ch), src, live);
+                row += kRowStep;
+                R += kRowStep;
+                tok += tok_step;
+                gq += g_step;
+                if (gq >= G) {
+                    gq -= G;
+                    ++tok;
+                }
+            }
+        };
+        auto publish_q = [&](int buf) {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_q(buf, gr));
+        };
+        auto next_item = [&](long long& r, Item& w) {        // the CTA's next item with rows for this group
+            for (long long i = item_index(++r); i < n_items; i = item_index(++r))
+                if (get_item(p, i, w, tile0) == 1 && w.nt[gr] > 0) return true;
+            return false;
+        };
+        long long r = -1;
+        Item it, nx;
+        bool has = next_item(r, it), failed = false;
+        if (has) {
+            load_q(it, 0);
+            publish_q(0);
+        }
+        int tt = 0, k = 0;                                   // tiles and items so far
+        while (has && !failed) {
+            const bool has_nx = next_item(r, nx);
+            if (has_nx) load_q(nx, (k + 1) & 1);
+            const int R = it.r0 + gr * kRows + tr, L = it.L, nt = it.nt[gr];
+            const int pos = R < it.rows ? L - it.Tq + R / G : L - 1;   // padded rows: computed, not written
+            const int pos_first = L - it.Tq + (it.r0 + gr * kRows) / G;
+            float m_run = -INFINITY, l_run = 0.f;
+            for (int t = 0; t < nt; ++t, ++tt) {
+                if (!warp_wait(bar_s(gr), (uint32_t)(tt & 1), p.status)) {
+                    failed = true;
+                    break;
+                }
+                tc_fence_after_sync();
+                uint32_t sr[64];
+                tmem_ld64(t_lane + C::kColS + gr * 64, sr);
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_sf(gr));      // S may be overwritten
+                const int k0 = t * kKeys;
+                if (k0 + kKeys - 1 > pos_first) {            // a tile on the diagonal: mask
+#pragma unroll
+                    for (int j = 0; j < 64; ++j)
+                        if (k0 + j > pos) sr[j] = __float_as_uint(-INFINITY);
+                }
+                float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int j = 0; j < 64; j += 2)
+                    mq[(j >> 1) & 3] = fmax3(mq[(j >> 1) & 3], __uint_as_float(sr[j]), __uint_as_float(sr[j + 1]));
+                const float mx = fmax3(mq[0], mq[1], fmaxf(mq[2], mq[3]));
+                const float m_new = fmaxf(m_run, mx * sl2);  // finite: key 0 is in every row's range
+                if (t == 0) {
+                    m_run = m_new;
+                } else {
+                    const bool need = m_new > m_run + kRescaleLog2;
+                    if (__any_sync(0xffffffffu, need)) {
+                        if (!wait_o(tt - 1)) {               // O holds the previous tile in full
+                            failed = true;
+                            break;
+                        }
+                        tc_fence_after_sync();
+                        const float a = need ? fast_exp2(m_run - m_new) : 1.f;
+#pragma unroll
+                        for (int h = 0; h < D / 32; ++h) tmem_scale32(t_lane + C::kColO + gr * D + h * 32, a);
+                        if (need) {
+                            l_run *= a;
+                            m_run = m_new;
+                        }
+                    }
+                }
+                const uint64_t sc2 = f2(sl2, sl2), nm2 = f2(-m_run, -m_run);
+                uint64_t rs2[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+                uint32_t pk[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    float x0, x1;
+                    f2_split(f2_fma(f2(__uint_as_float(sr[2 * j]), __uint_as_float(sr[2 * j + 1])), sc2, nm2), x0, x1);
+                    const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+                    rs2[j & 1] = f2_add(rs2[j & 1], f2(p0, p1));
+                    pk[j] = pack_f16x2(p0, p1);
+                }
+                float r0a, r0b, r1a, r1b;
+                f2_split(rs2[0], r0a, r0b);
+                f2_split(rs2[1], r1a, r1b);
+                l_run += (r0a + r1a) + (r0b + r1b);
+                if (t > 0 && !wait_o(tt - 1)) {              // the P V that read the P buffer is done
+                    failed = true;
+                    break;
+                }
+                tmem_st32(t_lane + C::kColP + gr * 32, pk);
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_p(gr));
+            }
+            if (failed || !wait_o(tt - 1)) {
+                failed = true;
+                break;
+            }
+            tc_fence_after_sync();
+            const int tok = R / G, gq = R - tok * G;
+            const float inv = p.out_scale / l_run;
+            uint16_t* out = p.out + ((size_t)(it.q0 + tok) * Hq + (size_t)it.kvh * G + gq) * D;
+#pragma unroll
+            for (int h = 0; h < D / 32; ++h) {
+                uint32_t o[32];
+                tmem_ld32(t_lane + C::kColO + gr * D + h * 32, o);   // warp-wide: padded rows join the load
+                if (R < it.rows) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint4 w;
+                        w.x = pack_bf16x2(__uint_as_float(o[8 * c + 0]) * inv, __uint_as_float(o[8 * c + 1]) * inv);
+                        w.y = pack_bf16x2(__uint_as_float(o[8 * c + 2]) * inv, __uint_as_float(o[8 * c + 3]) * inv);
+                        w.z = pack_bf16x2(__uint_as_float(o[8 * c + 4]) * inv, __uint_as_float(o[8 * c + 5]) * inv);
+                        w.w = pack_bf16x2(__uint_as_float(o[8 * c + 6]) * inv, __uint_as_float(o[8 * c + 7]) * inv);
+                        *reinterpret_cast<uint4*>(out + h * 32 + 8 * c) = w;
+                    }
+                }
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_of(gr));
+            if (has_nx) publish_q((k + 1) & 1);
+            ++k;
+            it = nx;
+            has = has_nx;
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");     // nothing left in flight at exit
+    }
+    // every role is done issuing: the MMA thread waits for its own MMAs
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == kMmaWarp && lane == 0) {
+        umma_commit(bar_drain);
+        mbar_wait(bar_drain, 0u, p.status);
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, C::kTmemCols);
+    }
+}
+
+template <int D>
+cudaError_t launch_p(const PrefillParams& p, int max_q_len, cudaStream_t stream) {
+    constexpr size_t smem = PCfg<D>::kSmem;
+    static std::atomic<uint64_t> attr_set{0};               // one bit per device
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!(attr_set.load(std::memory_order_acquire) & (1ull << dev))) {
+        cudaFuncAttributes fa;                              // the register shares count on the launch's number
+        if (cudaFuncGetAttributes(&fa, prefill_e2m1_kernel<D>) != cudaSuccess || fa.numRegs != kLaunchRegs)
+            return cudaErrorInvalidConfiguration;
+        const cudaError_t e =
+            cudaFuncSetAttribute(prefill_e2m1_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        attr_set.fetch_or(1ull << dev, std::memory_order_acq_rel);
+    }
+    int sms = 0;
+    if (num_sms_current_device(&sms) != PA_OK || sms <= 0) return cudaErrorInvalidDevice;
+    const long long tiles = ((long long)max_q_len * p.group + kItemRows - 1) / kItemRows;
+    const long long items = (long long)p.num_seqs * p.num_kv_heads * tiles;
+    if (items <= 0) return cudaSuccess;
+    prefill_e2m1_kernel<D><<<(unsigned)std::min<long long>(items, sms), kThreads, smem, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_e2m1(const PrefillParams& p, int max_q_len, cudaStream_t stream) {
+    if (p.head_dim == 64) return launch_p<64>(p, max_q_len, stream);
+    if (p.head_dim == 128) return launch_p<128>(p, max_q_len, stream);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace pa
