@@ -124,6 +124,10 @@ int make_decode_plan(int32_t num_seqs, int32_t max_context_len, const pa_cache_d
         if (plan->grid <= 0) return PA_ERR_CUDA;
         plan->desc_heads = e2m1_head_group(d.num_kv_heads);
         plan->slices = plan->grid * (8 / plan->desc_heads);
+        // a slice's slabs are counted in 32 bits
+        if ((int64_t)num_seqs * (d.num_kv_heads / plan->desc_heads) * (max_context_len / 16 + 1) / plan->slices >=
+            (int64_t)INT32_MAX)
+            return PA_ERR_UNSUPPORTED;
         plan->off_lse = plan->off_desc + up((size_t)(d.num_kv_heads / plan->desc_heads) * num_seqs * 16);
         const size_t rows = (size_t)plan->slices * 2 * d.num_kv_heads * G;
         plan->off_o = plan->off_lse + up(rows * sizeof(float));

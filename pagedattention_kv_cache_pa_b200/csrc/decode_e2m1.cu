@@ -4,9 +4,10 @@
 // bf16.  At that size a decode is no longer bound by its bytes alone: every code has to be widened
 // and scaled before a tensor core can take it, so the kernel is built around that work.
 //
-//  * A warp owns one kv head of a run of tokens and keeps everything in registers: the codes of 16
-//    tokens come straight from global memory in the shape of the MMA operands (no shared memory,
-//    no barrier, nothing to wait for but the loads themselves), a few slabs ahead of their use.
+//  * A warp owns one kv head of a run of tokens, copies its pages into a ring of its own in shared
+//    memory (16-byte asynchronous copies, a few slabs ahead) and takes the codes from there in the
+//    shape of the MMA operands: no barrier, no other warp to wait for.  Held in registers instead,
+//    the slabs ahead were one at most, and the loads' latency half of the time.
 //  * S = K q^T (16 tokens x 8 heads) takes K as the row operand: lane (r, c) holds, of tokens
 //    tau(r) and tau(r) + 2, the c-th quarter of the head dimension, which is one load of whole
 //    scale groups; the order of the dims inside the product is free, so q is laid out to match.
@@ -47,25 +48,52 @@ template <int D, int NT>
 struct ECfg {
     static constexpr int kTiles = D == 64 ? 2 : 1;          // 16-token tiles a slab
     static constexpr int kSlab = 16 * kTiles;
-    static constexpr int kBufs = D == 64 ? 2 : 3;           // slabs in registers
+    static constexpr int kStages = 4;                       // slabs of a warp's ring
     static constexpr int kW = D / 64;                       // words of 8 codes a lane and token (V); half of K's
     static constexpr int kSteps = D / 16;                   // k steps of S, m tiles of O
     static constexpr int kMinBlocks = NT == 1 ? 2 : 1;
+    // a stage: K codes, V codes, then per tile the scales of K and of V
+    static constexpr int kCodeBytes = kSlab * D / 2, kTileScales = D;
+    static constexpr int kStageBytes = 2 * kCodeBytes + 2 * kTiles * kTileScales;
+    static constexpr size_t kSmem = (size_t)kWarps * kStages * kStageBytes;
 };
 
-// What a lane holds of a slab, and what the slab is.
-template <int D, int NT>
+// What a slab is (kept beside its bytes).
 struct ESlab {
-    using C = ECfg<D, NT>;
-    uint32_t kc[C::kTiles][2][2 * C::kW];   // K codes of tokens tau(r), tau(r) + 2
-    uint32_t ks[C::kTiles][C::kW];          // their group scales, four tokens a word
-    uint32_t vc[C::kTiles][4][C::kW];       // V codes of tokens 4c .. 4c+3
-    uint32_t vs[C::kTiles];                 // their scales
-    int32_t b, valid;                       // sequence; tokens of the slab (0: an empty sequence)
-    int32_t kvh;
+    int32_t b, kvh;
+    int32_t valid;                          // tokens (0: an empty sequence)
     int32_t flags;                          // kFirst, kLast; nsplit << 8; slot << 7
 };
 enum : int32_t { kFirst = 1, kLast = 2, kSlot1 = 128 };
+
+// 16-byte copies to shared memory, zeros instead where !live.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live = true) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t r;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 r;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 r;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+    return r;
+}
+
+// Where 16-byte chunk i of a tile's codes lies: chunks are permuted inside their 128-byte line so
+// that a warp's reads of either operand's shape touch every bank once.  D = 64 (4 tokens a line):
+// by 0, 4, 2, 6 from line to line; D = 128 (2 tokens a line): by 0, 0, 2, 2, 4, 4, 6, 6.
+template <int D>
+__device__ __forceinline__ uint32_t code_chunk(uint32_t i) {
+    const uint32_t line = i >> 3;
+    return D == 64 ? i ^ (((line & 1) << 2) | (line & 2)) : i ^ (line & 6);
+}
 
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
     float d;
@@ -87,11 +115,14 @@ __device__ __forceinline__ int32_t slice_of(int64_t s, int64_t S, int64_t G, boo
                  : (int32_t)(((s + 1) * G - 1) / S);
 }
 
-template <int D, int NT>
+// kSmall: pages of 8 tokens (a 16-token tile spans two).
+template <int D, int NT, bool kSmall>
 __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
     decode_e2m1_kernel(const DecodeParams p, const int HG) {
     using C = ECfg<D, NT>;
     constexpr int SL = C::kSlab, TS = C::kTiles, W = C::kW;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ ESlab s_slab[kWarps][C::kStages];
     allow_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = lane >> 2, c = lane & 3;
@@ -100,7 +131,6 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
     const int hl = warp % HG, groups = Hkv / HG;
     const int64_t slice = (int64_t)blockIdx.x * (kWarps / HG) + warp / HG;
     const int64_t slices = (int64_t)gridDim.x * (kWarps / HG);
-    const size_t page_bytes = e2m1_page_bytes(Bs, D);
 
     // ---- the slice: lane i sums the slabs of sequences [i cs, (i + 1) cs), one scan joins them ----
     const int cs = (B + 31) / 32;
@@ -154,17 +184,26 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
     int32_t win_base = (j * SL) >> bs_shift;
     int32_t win = entry(b, win_base + lane), win2 = entry(b, win_base + 32 + lane);
     int32_t nx_len = 0, nx_win = -1;                        // the next sequence's length and first window
-    int64_t s = lo;
+    int32_t left = (int32_t)(hi - lo);                      // slabs to request (fits: checked on the host)
+    bool at_start = true;
     int32_t seg = 0;                                        // nsplit << 8 | slot << 7 of the current segment
 
-    const int tau = 4 * (r >> 1) + (r & 1);                 // K token of row r (the other is tau + 2)
-    const int k_quad = 4 * (r >> 1), v_quad = 4 * c;        // first token of the scale words
-    const uint32_t v_group = D == 64 ? r >> 1 : r;
-    uint8_t* const kc_base = reinterpret_cast<uint8_t*>(const_cast<uint16_t*>(p.k_cache));
-    uint8_t* const vc_base = reinterpret_cast<uint8_t*>(const_cast<uint16_t*>(p.v_cache));
+    const uint32_t page_bytes = (uint32_t)e2m1_page_bytes(Bs, D);
+    const uint8_t* const kc = reinterpret_cast<const uint8_t*>(p.k_cache);
+    const uint8_t* const vc = reinterpret_cast<const uint8_t*>(p.v_cache);
+    const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStageBytes;
+    ESlab* const slabs = s_slab[warp];
+    // this lane's scale copies: tile, cache, chunk of the tile's scales
+    constexpr int kScaleChunks = D / 16;
+    const int sc_u = lane / (2 * kScaleChunks), sc_v = (lane / kScaleChunks) & 1, sc_i = lane % kScaleChunks;
+    const int sc_tok = kSmall ? 8 * (sc_i / (kScaleChunks / 2)) : 0;                     // first token it covers
+    const uint32_t sc_off = Bs * (D / 2) + (kSmall ? (sc_i % (kScaleChunks / 2)) * 16 : sc_i * Bs);
+    const bool sc_on = sc_u < TS;
+    const uint8_t* const sc_src = (sc_v ? vc : kc) + sc_off;
+    const uint32_t sc_dst = 2 * C::kCodeBytes + lane * 16;
 
-    auto fetch = [&](ESlab<D, NT>& x) {
-        const bool first = s == lo || j == 0, last = s == hi - 1 || j == nb - 1;
+    auto fetch = [&](int st) {
+        const bool first = at_start || j == 0;
         if (first) {
             const int32_t i_first = slice_of(P, S, Gc, small), i_last = slice_of(P + nb - 1, S, Gc, small);
             const int32_t fslot = P < slice_lo(i_first, S, Gc, small) ? 0 : 1;
@@ -172,87 +211,60 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
             if (P >= lo && hl == 0 && lane == 0)            // this slice holds the sequence's first slab
                 reinterpret_cast<int4*>(p.seq_desc)[(size_t)gi * B + b] =
                     make_int4(i_last - i_first + 1, i_first, fslot, 0);
-            if (s != lo) {
+            if (!at_start) {
                 win_base = 0;
                 win = nx_win;
                 win2 = entry(b, 32 + lane);
             }
-            if (s + (nb - j) < hi) {                        // the slice reaches the next sequence
+            at_start = false;
+            if (lane < (G * D + 63) / 64)                   // its query rows, needed when it is processed
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + ((size_t)b * p.num_q_heads +
+                                                                     (size_t)(gi * HG + hl) * G) * D + lane * 64));
+            if (nb - j < left) {                            // the slice reaches the next sequence
                 const int32_t bn = b + 1 == B ? 0 : b + 1;
                 nx_len = __ldg(p.context_lens + bn);
                 nx_win = entry(bn, lane);
             }
         }
-        const int32_t t0 = j * SL;
-        x.b = b;
-        x.kvh = gi * HG + hl;
-        x.valid = L == 0 ? 0 : min(SL, L - t0);
-        x.flags = (first ? kFirst : 0) | (last ? kLast : 0) | seg;
+        const int32_t t0 = j * SL, kvh = gi * HG + hl;
+        if (lane == 0) {
+            const bool last = left == 1 || j == nb - 1;
+            slabs[st] = ESlab{b, kvh, min(SL, L - t0), (first ? kFirst : 0) | (last ? kLast : 0) | seg};
+        }
         if (((t0 >> bs_shift) - win_base) >= 32) {          // a slab's blocks never straddle windows
             win_base += 32;
             win = win2;
             win2 = entry(b, win_base + 32 + lane);
         }
+        // Every lane copies, whatever the slab holds: tokens past the sequence are masked later; a
+        // block outside the pool is read as block 0, with zeros for its scales.
+        const uint32_t dst = ring + st * C::kStageBytes;
+        bool bad = false;
 #pragma unroll
-        for (int u = 0; u < TS; ++u) {
-            const int tk = t0 + 16 * u + k_quad, tv = t0 + 16 * u + v_quad;
-            const int32_t bk = __shfl_sync(0xffffffffu, win, ((tk >> bs_shift) - win_base) & 31);
-            const int32_t bv = __shfl_sync(0xffffffffu, win, ((tv >> bs_shift) - win_base) & 31);
-            bool ok = tk < L, ov = tv < L;
-            if ((ok && (bk < 0 || bk >= p.num_blocks)) || (ov && (bv < 0 || bv >= p.num_blocks)))
-                raise_status(p.status, kStatusBadBlock);
-            ok = ok && bk >= 0 && bk < p.num_blocks;        // a block outside the pool reads as zeros
-            ov = ov && bv >= 0 && bv < p.num_blocks;
-#pragma unroll
-            for (int i = 0; i < W; ++i) x.ks[u][i] = 0u;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int i = 0; i < 2 * W; ++i) x.kc[u][h][i] = 0u;
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int i = 0; i < W; ++i) x.vc[u][t][i] = 0u;
-            x.vs[u] = 0u;
-            if (ok) {
-                const uint8_t* page = kc_base + ((size_t)bk * Hkv + x.kvh) * page_bytes;
-                const int off = tk & (Bs - 1);
-                const uint8_t* row = page + (off + (r & 1)) * (D / 2) + c * (D / 8);
-                if constexpr (D == 64) {
-                    const uint2 a0 = __ldcg(reinterpret_cast<const uint2*>(row));
-                    const uint2 a1 = __ldcg(reinterpret_cast<const uint2*>(row + 2 * (D / 2)));
-                    x.kc[u][0][0] = a0.x; x.kc[u][0][1] = a0.y;
-                    x.kc[u][1][0] = a1.x; x.kc[u][1][1] = a1.y;
-                } else {
-                    const uint4 a0 = __ldcg(reinterpret_cast<const uint4*>(row));
-                    const uint4 a1 = __ldcg(reinterpret_cast<const uint4*>(row + 2 * (D / 2)));
-                    x.kc[u][0][0] = a0.x; x.kc[u][0][1] = a0.y; x.kc[u][0][2] = a0.z; x.kc[u][0][3] = a0.w;
-                    x.kc[u][1][0] = a1.x; x.kc[u][1][1] = a1.y; x.kc[u][1][2] = a1.z; x.kc[u][1][3] = a1.w;
-                }
-                const uint8_t* sc = page + Bs * (D / 2) + off;
-#pragma unroll
-                for (int i = 0; i < W; ++i)
-                    x.ks[u][i] = __ldcg(reinterpret_cast<const uint32_t*>(sc + (c * W + i) * Bs));
-            }
-            if (ov) {
-                const uint8_t* page = vc_base + ((size_t)bv * Hkv + x.kvh) * page_bytes;
-                const int off = tv & (Bs - 1);
-                const uint8_t* row = page + off * (D / 2) + r * (D / 16);
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    if constexpr (D == 64) {
-                        x.vc[u][t][0] = __ldcg(reinterpret_cast<const uint32_t*>(row + t * (D / 2)));
-                    } else {
-                        const uint2 a = __ldcg(reinterpret_cast<const uint2*>(row + t * (D / 2)));
-                        x.vc[u][t][0] = a.x; x.vc[u][t][1] = a.y;
-                    }
-                }
-                uint32_t w = __ldcg(reinterpret_cast<const uint32_t*>(page + Bs * (D / 2) + v_group * Bs + off));
-                x.vs[u] = w;
-            }
+        for (int i = 0; i < TS * D / 64; ++i) {             // 32 chunks of codes, of K and of V
+            const uint32_t chunk = 32 * i + lane;
+            const int32_t tok = t0 + (int32_t)(chunk / (D / 32));
+            int32_t blk = __shfl_sync(0xffffffffu, win, ((tok >> bs_shift) - win_base) & 31);
+            const bool out = (uint32_t)blk >= (uint32_t)p.num_blocks;
+            bad |= out && tok < L;
+            blk = out ? 0 : blk;
+            const uint64_t off = (uint64_t)(uint32_t)(blk * Hkv + kvh) * page_bytes + (uint32_t)(tok & (Bs - 1)) * (D / 2) +
+                                 (chunk % (D / 32)) * 16;
+            const uint32_t at = dst + code_chunk<D>(chunk) * 16;
+            copy16(at, kc + off);
+            copy16(at + C::kCodeBytes, vc + off);
         }
+        {
+            const int32_t tok = t0 + 16 * sc_u + sc_tok;
+            const int32_t blk = __shfl_sync(0xffffffffu, win, ((tok >> bs_shift) - win_base) & 31);
+            const bool in = (uint32_t)blk < (uint32_t)p.num_blocks;
+            if (sc_on)
+                copy16(dst + sc_dst,
+                       sc_src + (uint64_t)(uint32_t)((in ? blk : 0) * Hkv + kvh) * page_bytes + (kSmall ? 0 : tok & (Bs - 1)), in);
+        }
+        if (bad) raise_status(p.status, kStatusBadBlock);
         // the next slab of the stream
-        ++s;
+        --left;
         if (++j == nb) {
             j = 0;
             P += nb;
@@ -260,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
                 b = 0;
                 ++gi;
             }
-            if (s < hi) {
+            if (left > 0) {
                 L = clip_length(p, nx_len);
                 nb = slabs_of(L);
             }
@@ -273,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
     float o_acc[NT][C::kSteps][4];
     const uint32_t sel = (r & 1) ? 0x3311u : 0x2200u;       // scales of tokens tau, tau + 2, each twice
 
-    auto start = [&](const ESlab<D, NT>& x) {
+    auto start = [&](const ESlab& x) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int h = nt * 8 + r;
@@ -295,8 +307,10 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
             const uint32_t e = __float_as_uint(big) >> 23;                    // biased exponent
             const uint32_t up = e < 9u ? 253u : 262u - e;                     // 2^(8 - (e - 127)), biased
-            const float f = __uint_as_float(up << 23);
-            const float back = p.scale_log2 * __uint_as_float((254u - up) << 23);   // 2^-(up - 127)
+            // the scale's sign goes with q, so that a larger product is a larger score
+            const float f = copysignf(__uint_as_float(up << 23), p.scale_log2);
+            // (never 0, which would turn a masked -inf into a NaN)
+            const float back = fmaxf(fabsf(p.scale_log2) * __uint_as_float((254u - up) << 23), 1e-37f);
 #pragma unroll
             for (int ks = 0; ks < C::kSteps; ++ks) {
                 qf[nt][ks][0] = pack_f16x2(bf16_lo(w[2 * ks]) * f, bf16_hi(w[2 * ks]) * f);
@@ -315,7 +329,28 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
         }
     };
 
-    auto process = [&](ESlab<D, NT>& x) {
+    // this lane's places in a stage
+    const int tau = 4 * (r >> 1) + (r & 1);                 // K token of row r (the other is tau + 2)
+    const int k_quad = 4 * (r >> 1), v_quad = 4 * c;        // first token of the scale words
+    constexpr int kTileCodes = 16 * D / 2;
+    uint32_t k_at[2], v_at[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        k_at[i] = D == 64 ? code_chunk<D>((tau + 2 * i) * 2 + (c >> 1)) * 16 + (c & 1) * 8
+                          : code_chunk<D>((tau + 2 * i) * 4 + c) * 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v_at[i] = C::kCodeBytes + (D == 64 ? code_chunk<D>((v_quad + i) * 2 + (r >> 2)) * 16 + (r & 3) * 4
+                                           : code_chunk<D>((v_quad + i) * 4 + (r >> 1)) * 16 + (r & 1) * 8);
+    // scales of group g, four tokens from `quad`: [g][16 tokens], or [page][g][8 tokens]
+    auto scale_at = [&](int g, int quad) {
+        return 2 * C::kCodeBytes + (kSmall ? (quad >> 3) * (D / 2) + g * 8 + (quad & 7) : g * 16 + quad);
+    };
+    const uint32_t ks_at = scale_at(c * W, k_quad), vs_at = scale_at(D == 64 ? r >> 1 : r, v_quad) + C::kTileScales;
+
+    auto process = [&](const ESlab& x, int st) {
+        const uint32_t stage = ring + st * C::kStageBytes;
+
         if (x.valid == 0) {                                 // an empty sequence: zeros
             store_zero_group(p, x.b, x.kvh, lane, 32);
             return;
@@ -325,46 +360,70 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
         float sv[TS][NT][4];
 #pragma unroll
         for (int u = 0; u < TS; ++u) {
+            uint32_t kw[2][2 * W];                          // codes of tokens tau, tau + 2
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sv[u][nt][e] = 0.f;
+            for (int h = 0; h < 2; ++h) {
+                if constexpr (D == 64) {
+                    const uint2 a = lds64(stage + k_at[h] + u * kTileCodes);
+                    kw[h][0] = a.x; kw[h][1] = a.y;
+                } else {
+                    const uint4 a = lds128(stage + k_at[h] + u * kTileCodes);
+                    kw[h][0] = a.x; kw[h][1] = a.y; kw[h][2] = a.z; kw[h][3] = a.w;
+                }
+            }
 #pragma unroll
             for (int i = 0; i < W; ++i) {                   // one scale group: 16 dims, 4 k steps
-                const uint32_t ss = __byte_perm(x.ks[u][i], 0u, sel);
+                const uint32_t ss = __byte_perm(lds32(stage + ks_at + 2 * u * C::kTileScales + i * (kSmall ? 8 : 16)), 0u, sel);
                 const uint32_t s0 = e4m3x2_to_f16x2(ss), s1 = e4m3x2_to_f16x2(ss >> 16);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     uint32_t lo4[4], hi4[4];
-                    e2m1x8_to_f16x2x4(x.kc[u][0][2 * i + half], lo4);
-                    e2m1x8_to_f16x2x4(x.kc[u][1][2 * i + half], hi4);
+                    e2m1x8_to_f16x2x4(kw[0][2 * i + half], lo4);
+                    e2m1x8_to_f16x2x4(kw[1][2 * i + half], hi4);
 #pragma unroll
                     for (int k2 = 0; k2 < 2; ++k2) {
                         const uint32_t a[4] = {mul_f16x2(lo4[2 * k2], s0), mul_f16x2(hi4[2 * k2], s1),
                                                mul_f16x2(lo4[2 * k2 + 1], s0), mul_f16x2(hi4[2 * k2 + 1], s1)};
                         const int ks = 4 * i + 2 * half + k2;
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma_f16_16816(sv[u][nt], a, qf[nt][ks][0], qf[nt][ks][1]);
+                        for (int nt = 0; nt < NT; ++nt)
+                            if (ks == 0) mma_f16_16816_zero(sv[u][nt], a, qf[nt][ks][0], qf[nt][ks][1]);
+                            else mma_f16_16816(sv[u][nt], a, qf[nt][ks][0], qf[nt][ks][1]);
                     }
                 }
             }
         }
         // ---- online softmax in the log2 domain, the running max kept lazily ----
+        uint32_t vs4[TS];
+#pragma unroll
+        for (int u = 0; u < TS; ++u) vs4[u] = lds32(stage + vs_at + 2 * u * C::kTileScales);
+        if (x.valid < SL) {
+            // tokens past the sequence: no weight; their V may hold any bytes, NaN scales among them
+#pragma unroll
+            for (int u = 0; u < TS; ++u) {
+                const bool v_lo = 16 * u + tau < x.valid, v_hi = 16 * u + tau + 2 < x.valid;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (!(e < 2 ? v_lo : v_hi)) sv[u][nt][e] = -INFINITY;
+                const int in = x.valid - 16 * u - v_quad;
+                if (in < 4) vs4[u] = in <= 0 ? 0u : vs4[u] & (0xFFFFFFFFu >> (32 - 8 * in));
+            }
+        }
         float mx[NT][2];
         bool need = false;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mx[nt][0] = mx[nt][1] = -INFINITY;
+        for (int nt = 0; nt < NT; ++nt) {
+            mx[nt][0] = fmaxf(sv[0][nt][0], sv[0][nt][2]);
+            mx[nt][1] = fmaxf(sv[0][nt][1], sv[0][nt][3]);
 #pragma unroll
-        for (int u = 0; u < TS; ++u) {
-            const bool v_lo = 16 * u + tau < x.valid, v_hi = 16 * u + tau + 2 < x.valid;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    sv[u][nt][e] = (e < 2 ? v_lo : v_hi) ? sv[u][nt][e] * sl2[nt][e & 1] : -INFINITY;
+            for (int u = 1; u < TS; ++u) {
                 mx[nt][0] = fmax3(mx[nt][0], sv[u][nt][0], sv[u][nt][2]);
                 mx[nt][1] = fmax3(mx[nt][1], sv[u][nt][1], sv[u][nt][3]);
             }
+            mx[nt][0] *= sl2[nt][0];                        // sl2 > 0
+            mx[nt][1] *= sl2[nt][1];
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -392,8 +451,10 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
         for (int u = 0; u < TS; ++u)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const float p0 = fast_exp2(sv[u][nt][0] - m_run[nt][0]), p1 = fast_exp2(sv[u][nt][1] - m_run[nt][1]);
-                const float p2 = fast_exp2(sv[u][nt][2] - m_run[nt][0]), p3 = fast_exp2(sv[u][nt][3] - m_run[nt][1]);
+                const float p0 = fast_exp2(fmaf(sv[u][nt][0], sl2[nt][0], -m_run[nt][0]));
+                const float p1 = fast_exp2(fmaf(sv[u][nt][1], sl2[nt][1], -m_run[nt][1]));
+                const float p2 = fast_exp2(fmaf(sv[u][nt][2], sl2[nt][0], -m_run[nt][0]));
+                const float p3 = fast_exp2(fmaf(sv[u][nt][3], sl2[nt][1], -m_run[nt][1]));
                 l_run[nt][0] += p0 + p2;
                 l_run[nt][1] += p1 + p3;
                 pb[u][nt][0] = movmatrix_trans(pack_f16x2(p0, p1));   // tokens 4c, 4c+1
@@ -402,15 +463,22 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
         // ---- O^T += V^T P ----
 #pragma unroll
         for (int u = 0; u < TS; ++u) {
-            // tokens past the sequence may hold any bytes, NaN scales among them: scale 0
-            const int left = x.valid - 16 * u - v_quad;
-            uint32_t vs = x.vs[u];
-            if (left < 4) vs = left <= 0 ? 0u : vs & (0xFFFFFFFFu >> (32 - 8 * left));
+            const uint32_t vs = vs4[u];
+            uint32_t vw[4][W];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                if constexpr (D == 64) {
+                    vw[t][0] = lds32(stage + v_at[t] + u * kTileCodes);
+                } else {
+                    const uint2 a = lds64(stage + v_at[t] + u * kTileCodes);
+                    vw[t][0] = a.x; vw[t][1] = a.y;
+                }
+            }
             const uint32_t s01 = e4m3x2_to_f16x2(vs), s23 = e4m3x2_to_f16x2(vs >> 16);
 #pragma unroll
             for (int i = 0; i < W; ++i) {
                 const uint32_t M = 0x0F0F0F0Fu;
-                const uint32_t w0 = x.vc[u][0][i], w1 = x.vc[u][1][i], w2 = x.vc[u][2][i], w3 = x.vc[u][3][i];
+                const uint32_t w0 = vw[0][i], w1 = vw[1][i], w2 = vw[2][i], w3 = vw[3][i];
                 uint32_t e01[4], d01[4], e23[4], d23[4];    // even and odd dims of token pairs
                 e2m1x8_to_f16x2x4((w0 & M) | ((w1 << 4) & ~M), e01);
                 e2m1x8_to_f16x2x4(((w0 >> 4) & M) | (w1 & ~M), d01);
@@ -467,19 +535,35 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
 
     // everything below reads or writes what the previous kernel on the stream may touch
     wait_prerequisite();
-    ESlab<D, NT> buf[C::kBufs];
-    const int64_t total = hi - lo;
+    const int32_t todo = left;
 #pragma unroll
-    for (int i = 0; i < C::kBufs; ++i)
-        if (i < total) fetch(buf[i]);
-    for (int64_t done = 0; done < total; done += C::kBufs) {
-#pragma unroll
-        for (int i = 0; i < C::kBufs; ++i) {
-            if (done + i >= total) break;
-            process(buf[i]);
-            if (s < hi) fetch(buf[i]);
-        }
+    for (int i = 0; i < C::kStages - 1; ++i) {
+        if (left > 0) fetch(i);
+        asm volatile("cp.async.commit_group;" ::: "memory");
     }
+    for (int32_t i = 0, st = 0; i < todo; ++i) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
+        __syncwarp();                                       // every lane's copies of slab i; slab i - 1 read by all
+        if (left > 0) fetch(st == 0 ? C::kStages - 1 : st - 1);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        const ESlab x = slabs[st];
+        process(x, st);
+        st = st + 1 == C::kStages ? 0 : st + 1;
+    }
+}
+
+template <int D, int NT, bool kSmall>
+bool ensure_smem() {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    const uint64_t bit = 1ull << dev;
+    if (done.load(std::memory_order_acquire) & bit) return true;
+    if (cudaFuncSetAttribute(decode_e2m1_kernel<D, NT, kSmall>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)ECfg<D, NT>::kSmem) != cudaSuccess)
+        return false;
+    done.fetch_or(bit, std::memory_order_acq_rel);
+    return true;
 }
 
 template <int D, int NT>
@@ -489,7 +573,9 @@ int occupancy() {
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
     int occ = cache[dev].load(std::memory_order_acquire);
     if (occ > 0) return occ;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, decode_e2m1_kernel<D, NT>, kThreads, 0) != cudaSuccess)
+    if (!ensure_smem<D, NT, false>() ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, decode_e2m1_kernel<D, NT, false>, kThreads,
+                                                      ECfg<D, NT>::kSmem) != cudaSuccess)
         return 0;
     cache[dev].store(occ, std::memory_order_release);
     return occ;
@@ -497,16 +583,20 @@ int occupancy() {
 
 template <int D, int NT>
 cudaError_t launch_e(const DecodeParams& p, int grid, bool pdl, cudaStream_t stream) {
+    const bool small = p.block_size < 16;
+    if (!(small ? ensure_smem<D, NT, true>() : ensure_smem<D, NT, false>())) return cudaErrorInvalidConfiguration;
+    const auto kernel = small ? decode_e2m1_kernel<D, NT, true> : decode_e2m1_kernel<D, NT, false>;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = ECfg<D, NT>::kSmem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, decode_e2m1_kernel<D, NT>, p, p.desc_heads);
+    return cudaLaunchKernelEx(&cfg, kernel, p, p.desc_heads);
 }
 
 }  // namespace
