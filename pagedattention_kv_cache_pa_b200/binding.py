@@ -199,14 +199,21 @@ def declared_symbols(header: str = HEADER) -> list:
 
 
 # ---- pointer marshalling ----------------------------------------------------------------
+# A decode step is a few microseconds on the GPU, so what is done per argument here counts: torch is
+# looked up once, and a well-formed tensor costs four attribute reads.
+_DTYPES: dict = {}          # torch dtypes by name, filled at the first tensor argument
+
+
+def _torch_dtype(name: str):
+    import torch
+    return _DTYPES.setdefault(name, getattr(torch, name))
+
+
 def _dev(t, dtype_name: str, what: str):
     """Device pointer of a contiguous CUDA tensor of the given torch dtype (or a raw int)."""
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
-    import torch
-    want = getattr(torch, dtype_name)
+    want = _DTYPES.get(dtype_name) or _torch_dtype(dtype_name)
     if t.dtype != want:
         raise TypeError("%s: expected %s, got %s" % (what, want, t.dtype))
     if not t.is_cuda:
@@ -221,12 +228,12 @@ def _cache(t, desc: "CacheDesc", what: str, options=None):
     options say so) that holds at least the pool desc describes."""
     kv_dtype = PA_KV_BF16 if options is None else options.kv_dtype
     if t is not None and not isinstance(t, int):
-        need = int(desc.num_blocks) * desc.num_kv_heads * desc.block_size * desc.head_dim
+        need = desc.num_blocks * desc.num_kv_heads * desc.block_size * desc.head_dim
         if kv_dtype == PA_KV_E2M1:
             need = need * 9 // 16
         if t.numel() < need:
             raise ValueError("%s holds %d elements, the pool described needs %d" % (what, t.numel(), need))
-    return _dev(t, "uint8" if kv_dtype in (PA_KV_E4M3, PA_KV_E2M1) else "bfloat16", what)
+    return _dev(t, "bfloat16" if kv_dtype == PA_KV_BF16 else "uint8", what)
 
 
 def _rows(t, num_tokens: int, heads: int, desc: "CacheDesc", what: str):
@@ -237,10 +244,24 @@ def _rows(t, num_tokens: int, heads: int, desc: "CacheDesc", what: str):
     return _dev(t, "bfloat16", what)
 
 
+_current_raw_stream = None   # of the current device, once torch is there
+
+
+def _find_raw_stream():
+    import torch
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    if raw is None or device is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    torch.cuda.init()
+    return lambda: raw(device())
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        global _current_raw_stream
+        if _current_raw_stream is None:
+            _current_raw_stream = _find_raw_stream()
+        return _current_raw_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

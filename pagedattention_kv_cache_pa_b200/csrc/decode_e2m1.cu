@@ -46,9 +46,10 @@ constexpr float kLazyLog2 = 8.f;      // a slab rescales O only when a score pas
 
 template <int D, int NT>
 struct ECfg {
-    static constexpr int kTiles = D == 64 ? 2 : 1;          // 16-token tiles a slab
+    static constexpr int kTiles = D == 64 ? 4 : 2;          // 16-token tiles a slab
     static constexpr int kSlab = 16 * kTiles;
-    static constexpr int kStages = 4;                       // slabs of a warp's ring
+    static constexpr int kStages = 3;                       // slabs of a warp's ring
+    static constexpr int kChunk = D == 64 ? 2 : 1;          // tiles processed at a time (the code of one turn)
     static constexpr int kW = D / 64;                       // words of 8 codes a lane and token (V); half of K's
     static constexpr int kSteps = D / 16;                   // k steps of S, m tiles of O
     static constexpr int kMinBlocks = NT == 1 ? 2 : 1;
@@ -62,9 +63,11 @@ struct ECfg {
 struct ESlab {
     int32_t b, kvh;
     int32_t valid;                          // tokens (0: an empty sequence)
-    int32_t flags;                          // kFirst, kLast; nsplit << 8; slot << 7
+    int32_t flags;                          // kFirst, kLast
+    int64_t P;                              // stream index of the sequence's slab 0
+    int32_t nb;                             // its slabs
 };
-enum : int32_t { kFirst = 1, kLast = 2, kSlot1 = 128 };
+enum : int32_t { kFirst = 1, kLast = 2 };
 
 // 16-byte copies to shared memory, zeros instead where !live.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live = true) {
@@ -106,7 +109,7 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     return r;
 }
 
-// CTA-slice arithmetic: slice i of G takes slabs [i S / G, (i + 1) S / G); in 32 bits where they hold it.
+// Slice i of G takes slabs [i S / G, (i + 1) S / G).  small (from the call's bounds): 32 bits hold S G.
 __device__ __forceinline__ int64_t slice_lo(int64_t i, int64_t S, int64_t G, bool small) {
     return small ? (int64_t)((uint32_t)i * (uint32_t)S / (uint32_t)G) : i * S / G;
 }
@@ -118,7 +121,7 @@ __device__ __forceinline__ int32_t slice_of(int64_t s, int64_t S, int64_t G, boo
 // kSmall: pages of 8 tokens (a 16-token tile spans two).
 template <int D, int NT, bool kSmall>
 __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
-    decode_e2m1_kernel(const DecodeParams p, const int HG) {
+    decode_e2m1_kernel(const DecodeParams p, const int HG, const bool small) {
     using C = ECfg<D, NT>;
     constexpr int SL = C::kSlab, TS = C::kTiles, W = C::kW;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -136,40 +139,45 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
     const int cs = (B + 31) / 32;
     const int c_lo = min(B, lane * cs), c_hi = min(B, c_lo + cs);
     auto slabs_of = [&](int32_t L) { return L == 0 ? 1 : (L + SL - 1) / SL; };
-    int64_t lane_sum = 0;
+    int64_t lane_sum = 0, incl;
+    if (small) {
+        uint32_t sum = 0;
 #pragma unroll 4
-    for (int b = c_lo; b < c_hi; ++b) lane_sum += slabs_of(clipped_length(p, b));
-    int64_t incl = lane_sum;
+        for (int b = c_lo; b < c_hi; ++b) sum += slabs_of(clipped_length(p, b));
+        uint32_t acc = sum;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += v;
+        for (int off = 1; off < 32; off <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, acc, off);
+            if (lane >= off) acc += v;
+        }
+        lane_sum = sum;
+        incl = acc;
+    } else {
+        for (int b = c_lo; b < c_hi; ++b) lane_sum += slabs_of(clipped_length(p, b));
+        incl = lane_sum;
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += v;
+        }
     }
-    const int64_t S_seq = __shfl_sync(0xffffffffu, incl, 31), S = S_seq * groups;
-    const int64_t Gc = S < slices ? S : slices;             // never more slices than slabs
-    const bool small = (S + 1) * (Gc + 1) < (1ll << 32);
+    const int64_t S_seq = small ? (int64_t)__shfl_sync(0xffffffffu, (uint32_t)incl, 31) : __shfl_sync(0xffffffffu, incl, 31);
+    const int64_t S = S_seq * groups, Gc = S < slices ? S : slices;   // never more slices than slabs
     if (slice >= Gc) return;
     const int64_t lo = slice_lo(slice, S, Gc, small), hi = slice_lo(slice + 1, S, Gc, small);
 
     // ---- where slab lo is: group gi, sequence b, slab j of it; P = stream index of b's slab 0 ----
-    int32_t gi = small ? (int32_t)((uint32_t)lo / (uint32_t)S_seq) : (int32_t)(lo / S_seq);
+    int32_t gi = groups == 1 ? 0 : small ? (int32_t)((uint32_t)lo / (uint32_t)S_seq) : (int32_t)(lo / S_seq);
     int32_t b = 0, j = 0;
     int64_t P = 0;
     {
         const int64_t rem = lo - (int64_t)gi * S_seq, excl = incl - lane_sum;
         const int k = __ffs(__ballot_sync(0xffffffffu, rem >= excl && rem < incl)) - 1;
+        b = c_lo;
+        int64_t acc = excl;
         if (lane == k) {
-            int64_t acc = excl;
-            for (int bb = c_lo; bb < c_hi; ++bb) {
-                const int n = slabs_of(clipped_length(p, bb));
-                if (rem < acc + n) {
-                    b = bb;
-                    j = (int32_t)(rem - acc);
-                    P = (int64_t)gi * S_seq + acc;
-                    break;
-                }
-                acc += n;
-            }
+            for (int n; rem >= acc + (n = slabs_of(clipped_length(p, b))); ++b) acc += n;
+            j = (int32_t)(rem - acc);
+            P = (int64_t)gi * S_seq + acc;
         }
         b = __shfl_sync(0xffffffffu, b, k);
         j = __shfl_sync(0xffffffffu, j, k);
@@ -186,7 +194,6 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
     int32_t nx_len = 0, nx_win = -1;                        // the next sequence's length and first window
     int32_t left = (int32_t)(hi - lo);                      // slabs to request (fits: checked on the host)
     bool at_start = true;
-    int32_t seg = 0;                                        // nsplit << 8 | slot << 7 of the current segment
 
     const uint32_t page_bytes = (uint32_t)e2m1_page_bytes(Bs, D);
     const uint8_t* const kc = reinterpret_cast<const uint8_t*>(p.k_cache);
@@ -198,19 +205,19 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
     const int sc_u = lane / (2 * kScaleChunks), sc_v = (lane / kScaleChunks) & 1, sc_i = lane % kScaleChunks;
     const int sc_tok = kSmall ? 8 * (sc_i / (kScaleChunks / 2)) : 0;                     // first token it covers
     const uint32_t sc_off = Bs * (D / 2) + (kSmall ? (sc_i % (kScaleChunks / 2)) * 16 : sc_i * Bs);
-    const bool sc_on = sc_u < TS;
+    constexpr int kScaleTiles = 32 / (2 * kScaleChunks), kScaleCopies = TS / kScaleTiles;   // tiles a copy, copies
+    static_assert(kScaleCopies * kScaleTiles == TS, "whole copies of scales");
     const uint8_t* const sc_src = (sc_v ? vc : kc) + sc_off;
     const uint32_t sc_dst = 2 * C::kCodeBytes + lane * 16;
+    constexpr int kTileCodes = 16 * D / 2;
+    const uint8_t *const kc_lane = kc + lane * 16, *const vc_lane = vc + lane * 16;
+    uint32_t code_at[D / 64];
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) code_at[i] = code_chunk<D>(32 * i + lane) * 16;
 
     auto fetch = [&](int st) {
         const bool first = at_start || j == 0;
         if (first) {
-            const int32_t i_first = slice_of(P, S, Gc, small), i_last = slice_of(P + nb - 1, S, Gc, small);
-            const int32_t fslot = P < slice_lo(i_first, S, Gc, small) ? 0 : 1;
-            seg = ((i_last - i_first + 1) << 8) | (P < lo ? 0 : kSlot1);
-            if (P >= lo && hl == 0 && lane == 0)            // this slice holds the sequence's first slab
-                reinterpret_cast<int4*>(p.seq_desc)[(size_t)gi * B + b] =
-                    make_int4(i_last - i_first + 1, i_first, fslot, 0);
             if (!at_start) {
                 win_base = 0;
                 win = nx_win;
@@ -229,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
         const int32_t t0 = j * SL, kvh = gi * HG + hl;
         if (lane == 0) {
             const bool last = left == 1 || j == nb - 1;
-            slabs[st] = ESlab{b, kvh, min(SL, L - t0), (first ? kFirst : 0) | (last ? kLast : 0) | seg};
+            slabs[st] = ESlab{b, kvh, min(SL, L - t0), (first ? kFirst : 0) | (last ? kLast : 0), P, nb};
         }
         if (((t0 >> bs_shift) - win_base) >= 32) {          // a slab's blocks never straddle windows
             win_base += 32;
@@ -241,26 +248,42 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
         const uint32_t dst = ring + st * C::kStageBytes;
         bool bad = false;
 #pragma unroll
-        for (int i = 0; i < TS * D / 64; ++i) {             // 32 chunks of codes, of K and of V
-            const uint32_t chunk = 32 * i + lane;
-            const int32_t tok = t0 + (int32_t)(chunk / (D / 32));
-            int32_t blk = __shfl_sync(0xffffffffu, win, ((tok >> bs_shift) - win_base) & 31);
-            const bool out = (uint32_t)blk >= (uint32_t)p.num_blocks;
-            bad |= out && tok < L;
-            blk = out ? 0 : blk;
-            const uint64_t off = (uint64_t)(uint32_t)(blk * Hkv + kvh) * page_bytes + (uint32_t)(tok & (Bs - 1)) * (D / 2) +
-                                 (chunk % (D / 32)) * 16;
-            const uint32_t at = dst + code_chunk<D>(chunk) * 16;
-            copy16(at, kc + off);
-            copy16(at + C::kCodeBytes, vc + off);
+        for (int u = 0; u < TS; ++u) {
+            if (kSmall) {                                   // pages of 8 tokens: two a tile
+                constexpr int kPageChunks = D / 4;          // chunks of codes of a page
+                const int32_t tok = t0 + 16 * u + (D == 64 ? 8 * (lane / kPageChunks) : 0);
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) {
+                    const int32_t blk = __shfl_sync(0xffffffffu, win, ((tok >> 3) + i - win_base) & 31);
+                    const bool out = (uint32_t)blk >= (uint32_t)p.num_blocks;
+                    bad |= out && tok + 8 * i < L;
+                    const uint64_t off = (uint64_t)(uint32_t)((out ? 0 : blk) * Hkv + kvh) * page_bytes;
+                    const uint32_t at = dst + u * kTileCodes + code_at[i];
+                    copy16(at, kc + off + (lane % kPageChunks) * 16);
+                    copy16(at + C::kCodeBytes, vc + off + (lane % kPageChunks) * 16);
+                }
+            } else {
+                const int32_t tok = t0 + 16 * u;
+                const int32_t blk = __shfl_sync(0xffffffffu, win, ((tok >> bs_shift) - win_base) & 31);
+                const bool out = (uint32_t)blk >= (uint32_t)p.num_blocks;
+                bad |= out && tok < L;
+                const uint64_t off = (uint64_t)(uint32_t)((out ? 0 : blk) * Hkv + kvh) * page_bytes +
+                                     (uint32_t)(tok & (Bs - 1)) * (D / 2);
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) {          // 32 chunks of codes, of K and of V
+                    const uint32_t at = dst + u * kTileCodes + code_at[i];
+                    copy16(at, kc_lane + off + 512 * i);
+                    copy16(at + C::kCodeBytes, vc_lane + off + 512 * i);
+                }
+            }
         }
-        {
-            const int32_t tok = t0 + 16 * sc_u + sc_tok;
+#pragma unroll
+        for (int w = 0; w < kScaleCopies; ++w) {
+            const int32_t tok = t0 + 16 * (sc_u + w * kScaleTiles) + sc_tok;
             const int32_t blk = __shfl_sync(0xffffffffu, win, ((tok >> bs_shift) - win_base) & 31);
             const bool in = (uint32_t)blk < (uint32_t)p.num_blocks;
-            if (sc_on)
-                copy16(dst + sc_dst,
-                       sc_src + (uint64_t)(uint32_t)((in ? blk : 0) * Hkv + kvh) * page_bytes + (kSmall ? 0 : tok & (Bs - 1)), in);
+            copy16(dst + sc_dst + 512 * w,
+                   sc_src + (uint64_t)(uint32_t)((in ? blk : 0) * Hkv + kvh) * page_bytes + (kSmall ? 0 : tok & (Bs - 1)), in);
         }
         if (bad) raise_status(p.status, kStatusBadBlock);
         // the next slab of the stream
@@ -280,6 +303,7 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
     };
 
     // ---- state of the current segment ----
+    int32_t seg_split = 1, seg_slot = 0;
     uint32_t qf[NT][C::kSteps][2];
     float sl2[NT][2], m_run[NT][2], l_run[NT][2];
     float o_acc[NT][C::kSteps][4];
@@ -332,7 +356,6 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
     // this lane's places in a stage
     const int tau = 4 * (r >> 1) + (r & 1);                 // K token of row r (the other is tau + 2)
     const int k_quad = 4 * (r >> 1), v_quad = 4 * c;        // first token of the scale words
-    constexpr int kTileCodes = 16 * D / 2;
     uint32_t k_at[2], v_at[4];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -349,31 +372,45 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
     const uint32_t ks_at = scale_at(c * W, k_quad), vs_at = scale_at(D == 64 ? r >> 1 : r, v_quad) + C::kTileScales;
 
     auto process = [&](const ESlab& x, int st) {
-        const uint32_t stage = ring + st * C::kStageBytes;
+        constexpr int CT = C::kChunk;
+        uint32_t stage_codes = ring + st * C::kStageBytes, stage_scales = stage_codes;
 
-        if (x.valid == 0) {                                 // an empty sequence: zeros
+        if (x.valid == 0) {                                 // an empty sequence: zeros, nothing to join
             store_zero_group(p, x.b, x.kvh, lane, 32);
+            if (hl == 0 && lane == 0)
+                reinterpret_cast<int4*>(p.seq_desc)[(size_t)(x.kvh / HG) * B + x.b] = make_int4(1, 0, 0, 0);
             return;
         }
-        if (x.flags & kFirst) start(x);
+        if (x.flags & kFirst) {
+            start(x);
+            // the segment: how many slices share its sequence, and this one's partial slot
+            const int32_t i_first = slice_of(x.P, S, Gc, small), i_last = slice_of(x.P + x.nb - 1, S, Gc, small);
+            seg_split = i_last - i_first + 1;
+            seg_slot = x.P < lo ? 0 : 1;
+            if (x.P >= lo && hl == 0 && lane == 0)          // this slice holds the sequence's first slab
+                reinterpret_cast<int4*>(p.seq_desc)[(size_t)(x.kvh / HG) * B + x.b] =
+                    make_int4(seg_split, i_first, x.P < slice_lo(i_first, S, Gc, small) ? 0 : 1, 0);
+        }
+#pragma unroll 1
+        for (int valid = x.valid; valid > 0; valid -= 16 * CT, stage_codes += CT * kTileCodes, stage_scales += 2 * CT * C::kTileScales) {
         // ---- S = K q^T ----
-        float sv[TS][NT][4];
+        float sv[CT][NT][4];
 #pragma unroll
-        for (int u = 0; u < TS; ++u) {
+        for (int u = 0; u < CT; ++u) {
             uint32_t kw[2][2 * W];                          // codes of tokens tau, tau + 2
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 if constexpr (D == 64) {
-                    const uint2 a = lds64(stage + k_at[h] + u * kTileCodes);
+                    const uint2 a = lds64(stage_codes + k_at[h] + u * kTileCodes);
                     kw[h][0] = a.x; kw[h][1] = a.y;
                 } else {
-                    const uint4 a = lds128(stage + k_at[h] + u * kTileCodes);
+                    const uint4 a = lds128(stage_codes + k_at[h] + u * kTileCodes);
                     kw[h][0] = a.x; kw[h][1] = a.y; kw[h][2] = a.z; kw[h][3] = a.w;
                 }
             }
 #pragma unroll
             for (int i = 0; i < W; ++i) {                   // one scale group: 16 dims, 4 k steps
-                const uint32_t ss = __byte_perm(lds32(stage + ks_at + 2 * u * C::kTileScales + i * (kSmall ? 8 : 16)), 0u, sel);
+                const uint32_t ss = __byte_perm(lds32(stage_scales + ks_at + 2 * u * C::kTileScales + i * (kSmall ? 8 : 16)), 0u, sel);
                 const uint32_t s0 = e4m3x2_to_f16x2(ss), s1 = e4m3x2_to_f16x2(ss >> 16);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
@@ -394,20 +431,20 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
             }
         }
         // ---- online softmax in the log2 domain, the running max kept lazily ----
-        uint32_t vs4[TS];
+        uint32_t vs4[CT];
 #pragma unroll
-        for (int u = 0; u < TS; ++u) vs4[u] = lds32(stage + vs_at + 2 * u * C::kTileScales);
-        if (x.valid < SL) {
+        for (int u = 0; u < CT; ++u) vs4[u] = lds32(stage_scales + vs_at + 2 * u * C::kTileScales);
+        if (valid < 16 * CT) {
             // tokens past the sequence: no weight; their V may hold any bytes, NaN scales among them
 #pragma unroll
-            for (int u = 0; u < TS; ++u) {
-                const bool v_lo = 16 * u + tau < x.valid, v_hi = 16 * u + tau + 2 < x.valid;
+            for (int u = 0; u < CT; ++u) {
+                const bool v_lo = 16 * u + tau < valid, v_hi = 16 * u + tau + 2 < valid;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (!(e < 2 ? v_lo : v_hi)) sv[u][nt][e] = -INFINITY;
-                const int in = x.valid - 16 * u - v_quad;
+                const int in = valid - 16 * u - v_quad;
                 if (in < 4) vs4[u] = in <= 0 ? 0u : vs4[u] & (0xFFFFFFFFu >> (32 - 8 * in));
             }
         }
@@ -418,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
             mx[nt][0] = fmaxf(sv[0][nt][0], sv[0][nt][2]);
             mx[nt][1] = fmaxf(sv[0][nt][1], sv[0][nt][3]);
 #pragma unroll
-            for (int u = 1; u < TS; ++u) {
+            for (int u = 1; u < CT; ++u) {
                 mx[nt][0] = fmax3(mx[nt][0], sv[u][nt][0], sv[u][nt][2]);
                 mx[nt][1] = fmax3(mx[nt][1], sv[u][nt][1], sv[u][nt][3]);
             }
@@ -446,9 +483,9 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
                     }
                 }
         }
-        uint32_t pb[TS][NT][2];
+        uint32_t pb[CT][NT][2];
 #pragma unroll
-        for (int u = 0; u < TS; ++u)
+        for (int u = 0; u < CT; ++u)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const float p0 = fast_exp2(fmaf(sv[u][nt][0], sl2[nt][0], -m_run[nt][0]));
@@ -462,15 +499,15 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
             }
         // ---- O^T += V^T P ----
 #pragma unroll
-        for (int u = 0; u < TS; ++u) {
+        for (int u = 0; u < CT; ++u) {
             const uint32_t vs = vs4[u];
             uint32_t vw[4][W];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 if constexpr (D == 64) {
-                    vw[t][0] = lds32(stage + v_at[t] + u * kTileCodes);
+                    vw[t][0] = lds32(stage_codes + v_at[t] + u * kTileCodes);
                 } else {
-                    const uint2 a = lds64(stage + v_at[t] + u * kTileCodes);
+                    const uint2 a = lds64(stage_codes + v_at[t] + u * kTileCodes);
                     vw[t][0] = a.x; vw[t][1] = a.y;
                 }
             }
@@ -493,6 +530,7 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
                 }
             }
         }
+        }
         if (!(x.flags & kLast)) return;
         // ---- end of the segment: write out, or leave a partial state ----
 #pragma unroll
@@ -502,8 +540,8 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1)
                     l_run[nt][jj] += __shfl_xor_sync(0xffffffffu, l_run[nt][jj], off);
-        const bool whole = (x.flags >> 8) == 1;
-        const size_t prow = (((size_t)slice * 2 + ((x.flags & kSlot1) ? 1 : 0)) * Hkv + x.kvh) * G;
+        const bool whole = seg_split == 1;
+        const size_t prow = (((size_t)slice * 2 + seg_slot) * Hkv + x.kvh) * G;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -596,7 +634,11 @@ cudaError_t launch_e(const DecodeParams& p, int grid, bool pdl, cudaStream_t str
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, p, p.desc_heads);
+    // slabs of the whole call at most, times its slices: where that fits, the plan is made in 32 bits
+    const uint64_t slabs = (uint64_t)p.num_seqs * (p.num_kv_heads / p.desc_heads) *
+                           ((uint64_t)p.max_context_len / ECfg<D, NT>::kSlab + 1);
+    const bool fits = (slabs + 1) * ((uint64_t)p.grid + 1) < (1ull << 32);
+    return cudaLaunchKernelEx(&cfg, kernel, p, p.desc_heads, fits);
 }
 
 }  // namespace
