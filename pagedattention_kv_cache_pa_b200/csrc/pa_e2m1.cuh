@@ -135,9 +135,6 @@ __device__ __forceinline__ uint8_t* e2m1_scale(uint8_t* page, int block_size, in
 // RoPE for rows that are quantized after it.  A rotated value next to a border between two codes
 // must fall on the same side wherever it is computed, so the angle, its cosine and sine and the
 // rotation are all formed in double and the row is rounded to float, then to bf16.
-__device__ __forceinline__ double rope_inv_freq64(int i, int D, float theta) {
-    return pow((double)theta, -2.0 * (double)i / (double)D);
-}
 __device__ __forceinline__ void rope_cos_sin64(int32_t pos, double inv_freq, double* c, double* s) {
     const double a = (double)pos * inv_freq;
     // a - k 2 pi with 2 pi in two parts: |a| reaches 2^31, where one double of 2 pi is not enough
