@@ -359,6 +359,7 @@ PA_API int pa_append_decode(const pa_bf16* q, const pa_bf16* k, const pa_bf16* v
 #define PA_PREFILL_TCGEN05_WS 3   /* tcgen05 with one job per warp (softmax, MMA issue, TMA) and */
                                   /* O accumulated in tensor memory; block sizes 8, 16, 32, 64  */
                                   /* or multiples of 64 (PA_ERR_UNSUPPORTED otherwise)          */
+#define PA_PREFILL_ROWS 4         /* pa_prefill_ex over 4-bit pools only, see there             */
 PA_API int pa_prefill(const pa_bf16* q, const pa_bf16* k_cache, const pa_bf16* v_cache,
                       const int32_t* block_tables, const int32_t* cu_seqlens_q,
                       const int32_t* context_lens, int32_t num_seqs, int32_t max_q_len, float scale,
@@ -368,9 +369,12 @@ PA_API int pa_prefill(const pa_bf16* q, const pa_bf16* k_cache, const pa_bf16* v
 /*
  * pa_prefill over a cache of any built type.  options (NULL: all zero): kernel as for
  * pa_prefill; kv_dtype PA_KV_BF16 or PA_KV_E2M1 (4-bit pools, see pa_append_kv_e2m1, with
- * their scales; kernel PA_PREFILL_AUTO or PA_PREFILL_TCGEN05_WS, block sizes of 4-bit pools).
- * 4-bit K is widened to bf16 and V to f16 exactly, P is rounded to f16.  max_context_len: an
- * upper bound of every context_lens[b].  workspace: pa_prefill_workspace_size bytes,
+ * their scales; block sizes of 4-bit pools; kernel PA_PREFILL_TCGEN05_WS: tiles of 256 query
+ * rows; PA_PREFILL_ROWS: the decode kernel with several rows' heads for its columns, Hq / Hkv <= 16;
+ * PA_PREFILL_AUTO: the latter for few rows).
+ * 4-bit K is widened to bf16 (rows: f16, as q is after a power of two per row) and V to f16
+ * exactly, P is rounded to f16.  max_context_len: an upper bound of every context_lens[b] (a longer
+ * sequence may be reported as a bad length).  workspace: pa_prefill_workspace_size bytes,
  * 256-byte aligned, zero-filled before its first use, one per call in flight.  The rest, and
  * the errors, as for pa_prefill; also PA_ERR_UNSUPPORTED for PA_KV_E4M3.
  */
@@ -381,6 +385,8 @@ typedef struct pa_prefill_options {
     float v_scale;       /* PA_KV_E2M1: scale of the V cache tensor (> 0)                     */
 } pa_prefill_options;
 
+/* Bytes of workspace pa_prefill_ex needs for these arguments (0 on bad ones; needs a current CUDA
+ * device for 4-bit pools). */
 PA_API size_t pa_prefill_workspace_size(int32_t num_seqs, int32_t max_q_len, int32_t max_context_len,
                                         const pa_cache_desc* desc, const pa_prefill_options* options);
 PA_API int pa_prefill_ex(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,

@@ -10,7 +10,7 @@ from .binding import (  # noqa: F401
     pa_decode_max_splits, pa_decode_noalloc, pa_decode_status, pa_decode_workspace_size, pa_rope_append_kv,
     pa_slot_mapping,
     pa_status_string,
-    PrefillOptions, pa_prefill_ex, pa_prefill_workspace_size,
+    PA_PREFILL_ROWS, PrefillOptions, pa_prefill_ex, pa_prefill_workspace_size,
     pa_cross_attention, pa_cross_attention_workspace_size,
     pa_append_kv_e2m1, pa_copy_blocks_e2m1, pa_gather_kv_e2m1, pa_kv_cache_bytes, pa_rope_append_kv_e2m1,
 )

@@ -120,7 +120,7 @@ int make_decode_plan(int32_t num_seqs, int32_t max_context_len, const pa_cache_d
     if (opt && opt->kv_dtype == PA_KV_E2M1) {   // 4-bit pools: their own tensor kernel, any Hkv
         if (kernel != PA_KERNEL_TENSOR) return PA_ERR_UNSUPPORTED;
         plan->kernel = DecodeKernel::kE2m1;
-        plan->grid = e2m1_kernel_grid(d, opt->max_ctas);
+        plan->grid = e2m1_kernel_grid(d, G, opt->max_ctas);
         if (plan->grid <= 0) return PA_ERR_CUDA;
         plan->desc_heads = e2m1_head_group(d.num_kv_heads);
         plan->slices = plan->grid * (8 / plan->desc_heads);
@@ -506,6 +506,9 @@ static int decode_call(const pa_bf16* q, const pa_bf16* k_new, const pa_bf16* v_
     DecodeParams p;
     p.grid = plan.slices;
     p.desc_heads = plan.desc_heads;
+    p.cols = desc->num_q_heads / desc->num_kv_heads;
+    p.cu_q = nullptr;
+    p.q_tokens = p.q_chunks = p.max_q_len = 1;
     p.selftest_stall = stall ? 1 : 0;
     p.wait_ns = stall ? kSelftestWaitNs : kDecodeWaitNs;
     p.q = q;
@@ -606,14 +609,57 @@ extern "C" int pa_decode(const pa_bf16* q, const pa_bf16* k_cache, const pa_bf16
                         stream);
 }
 
+// Few rows a sequence over 4-bit pools run the decode kernel: columns are (token, query head) pairs,
+// at most 16 a kv head, and a sequence with more rows is several sequences of the stream.
+struct RowsPlan {
+    int32_t tokens, chunks, cols, grid, slices, desc_heads;
+    size_t off_lse, off_o, bytes;
+};
+
+static bool rows_plan(int32_t num_seqs, int32_t max_q_len, const pa_cache_desc& d, RowsPlan* r) {
+    const int32_t G = d.num_q_heads / d.num_kv_heads;
+    if (G > 16 || max_q_len < 1) return false;
+    r->tokens = 16 / G < max_q_len ? 16 / G : max_q_len;
+    r->chunks = (max_q_len + r->tokens - 1) / r->tokens;
+    r->cols = r->tokens * G;
+    r->grid = e2m1_kernel_grid(d, r->cols, 0);
+    if (r->grid <= 0) return false;
+    r->desc_heads = e2m1_head_group(d.num_kv_heads);
+    r->slices = r->grid * (8 / r->desc_heads);
+    auto up = [](size_t x) { return (x + kWorkspaceAlign - 1) / kWorkspaceAlign * kWorkspaceAlign; };
+    const size_t rows = (size_t)r->slices * 2 * d.num_kv_heads * r->cols;
+    r->off_lse = kWorkspaceAlign + up((size_t)(d.num_kv_heads / r->desc_heads) * num_seqs * r->chunks * 16);
+    r->off_o = r->off_lse + up(rows * sizeof(float));
+    r->bytes = r->off_o + up(rows * (size_t)d.head_dim * sizeof(float));
+    return true;
+}
+
+// Whether an automatic call of this shape takes it.  The rows' kernel reads and widens the keys once per
+// chunk of 16 columns, spread over all SMs (5.4 ns a key, chunk and SM); the tiles' kernel once per 256
+// rows, a kv head of a sequence to an SM at a time (18 ns a key and wave of items, 64- and 128-wide heads
+// alike).  Measured (us, rows' | tiles'), 32 query and 8 kv heads of 64: 1 x 2000 tokens, 16 rows 12.8 | 36.0;
+// 6 x 1000, 16 rows 21.3 | 21.2, 32 rows 27.1 | 21.7; 32 x 1000, 8 rows 30.0 | 40.2, 16 rows 47.7 | 39.9;
+// 64 x 2000, 8 rows 74 | 135, 16 rows 132 | 136; 64 and 8 heads of 128: 4 x 8000, 16 rows 112 | 158.  2.2 for
+// the ratio of 3.3 leaves short contexts, whose fixed costs weigh more, to the tiles.
+static bool rows_pay(int32_t num_seqs, int32_t max_q_len, const pa_cache_desc& d) {
+    const int32_t G = d.num_q_heads / d.num_kv_heads;
+    int sms = 0;
+    if (G > 16 || num_seqs < 1 || max_q_len < 1 || num_sms_current_device(&sms) != PA_OK) return false;
+    const int64_t pairs = (int64_t)num_seqs * d.num_kv_heads, chunks = ceil_div(max_q_len, 16 / G);
+    const int64_t waves = ceil_div(pairs * ceil_div((int64_t)max_q_len * G, 256), sms);
+    return 10 * chunks * pairs <= 22 * sms * waves;
+}
+
 static int check_prefill_options(const pa_prefill_options* o) {
     if (!o) return PA_OK;
-    if (o->kernel < PA_PREFILL_AUTO || o->kernel > PA_PREFILL_TCGEN05_WS) return PA_ERR_INVALID;
+    if (o->kernel < PA_PREFILL_AUTO || o->kernel > PA_PREFILL_ROWS) return PA_ERR_INVALID;
     if (o->kv_dtype == PA_KV_E4M3) return PA_ERR_UNSUPPORTED;
     if (o->kv_dtype == PA_KV_E2M1) {
         if (!good_scale(o->k_scale) || !good_scale(o->v_scale)) return PA_ERR_INVALID;
-        return o->kernel == PA_PREFILL_AUTO || o->kernel == PA_PREFILL_TCGEN05_WS ? PA_OK : PA_ERR_UNSUPPORTED;
+        return o->kernel == PA_PREFILL_AUTO || o->kernel == PA_PREFILL_TCGEN05_WS || o->kernel == PA_PREFILL_ROWS
+                   ? PA_OK : PA_ERR_UNSUPPORTED;
     }
+    if (o->kernel == PA_PREFILL_ROWS) return o->kv_dtype == PA_KV_BF16 ? PA_ERR_UNSUPPORTED : PA_ERR_INVALID;
     return o->kv_dtype == PA_KV_BF16 ? PA_OK : PA_ERR_INVALID;
 }
 
@@ -622,6 +668,12 @@ extern "C" size_t pa_prefill_workspace_size(int32_t num_seqs, int32_t max_q_len,
     if (check_desc(desc) != PA_OK || num_seqs < 0 || max_q_len < 0 || max_context_len < 0 ||
         check_prefill_options(options) != PA_OK)
         return 0;
+    if (options && options->kv_dtype == PA_KV_E2M1 &&
+        (options->kernel == PA_PREFILL_ROWS || (options->kernel == PA_PREFILL_AUTO && rows_pay(num_seqs, max_q_len, *desc)))) {
+        RowsPlan r;
+        if (check_e2m1_desc(desc) != PA_OK) return 0;
+        if (max_q_len > 0 && num_seqs > 0) return rows_plan(num_seqs, max_q_len, *desc, &r) ? r.bytes : 0;
+    }
     return kWorkspaceAlign;
 }
 
@@ -655,6 +707,49 @@ extern "C" int pa_prefill_ex(const void* q, const void* k_cache, const void* v_c
         return PA_ERR_INVALID;
     if (!workspace || !aligned(workspace, kWorkspaceAlign) || workspace_bytes < kWorkspaceAlign)
         return PA_ERR_WORKSPACE;
+    if (options->kernel == PA_PREFILL_ROWS || (options->kernel == PA_PREFILL_AUTO && rows_pay(num_seqs, max_q_len, *desc))) {
+        RowsPlan r;
+        if (desc->num_q_heads / desc->num_kv_heads > 16) return PA_ERR_UNSUPPORTED;
+        if (!rows_plan(num_seqs, max_q_len, *desc, &r)) return PA_ERR_CUDA;
+        if ((int64_t)num_seqs * r.chunks * (desc->num_kv_heads / r.desc_heads) * (max_context_len / 16 + 1) / r.slices >=
+            (int64_t)INT32_MAX)
+            return PA_ERR_UNSUPPORTED;
+        if (workspace_bytes < r.bytes) return PA_ERR_WORKSPACE;
+        char* ws = static_cast<char*>(workspace);
+        DecodeParams dp{};
+        dp.q = static_cast<const uint16_t*>(q);
+        dp.k_cache = static_cast<const uint16_t*>(k_cache);
+        dp.v_cache = static_cast<const uint16_t*>(v_cache);
+        dp.block_tables = block_tables;
+        dp.context_lens = context_lens;
+        dp.out = out;
+        dp.status = reinterpret_cast<int32_t*>(ws);
+        dp.seq_desc = reinterpret_cast<int32_t*>(ws + kWorkspaceAlign);
+        dp.part_lse = reinterpret_cast<float*>(ws + r.off_lse);
+        dp.part_o = reinterpret_cast<float*>(ws + r.off_o);
+        dp.num_seqs = num_seqs * r.chunks;
+        dp.num_blocks = desc->num_blocks;
+        dp.block_size = desc->block_size;
+        dp.num_kv_heads = desc->num_kv_heads;
+        dp.num_q_heads = desc->num_q_heads;
+        dp.head_dim = desc->head_dim;
+        dp.group = desc->num_q_heads / desc->num_kv_heads;
+        dp.max_blocks_per_seq = desc->max_blocks_per_seq;
+        dp.max_context_len = max_context_len;
+        dp.scale_log2 = scale * options->k_scale * 1.4426950408889634f;
+        dp.out_scale = options->v_scale;
+        dp.grid = r.slices;
+        dp.desc_heads = r.desc_heads;
+        dp.cols = r.cols;
+        dp.cu_q = cu_seqlens_q;
+        dp.q_tokens = r.tokens;
+        dp.q_chunks = r.chunks;
+        dp.max_q_len = max_q_len;
+        const cudaStream_t st = (cudaStream_t)stream;
+        cudaError_t e = launch_decode_e2m1(dp, r.grid, false, st);
+        if (e == cudaSuccess) e = launch_merge(dp, true, true, st);
+        return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    }
     PrefillParams p = prefill_params(q, k_cache, v_cache, block_tables, cu_seqlens_q, context_lens, num_seqs,
                                      max_q_len, scale * options->k_scale, out, workspace, *desc);
     p.out_scale = options->v_scale;

@@ -29,6 +29,7 @@
 // one cut between slices leaves fp32 partial states, two a slice at most, which the merge kernel
 // (merge.cu) joins.
 #include <cuda_runtime.h>
+#include <float.h>
 #include <stdint.h>
 
 #include <atomic>
@@ -62,7 +63,7 @@ struct ECfg {
 // What a slab is (kept beside its bytes).
 struct ESlab {
     int32_t b, kvh;
-    int32_t valid;                          // tokens (0: an empty sequence)
+    int32_t valid;                          // tokens of the sequence from the slab's first on (0: it is empty)
     int32_t flags;                          // kFirst, kLast
     int64_t P;                              // stream index of the sequence's slab 0
     int32_t nb;                             // its slabs
@@ -119,7 +120,10 @@ __device__ __forceinline__ int32_t slice_of(int64_t s, int64_t S, int64_t G, boo
 }
 
 // kSmall: pages of 8 tokens (a 16-token tile spans two).
-template <int D, int NT, bool kSmall>
+// kRows: causal prefill of few rows.  The columns of the products are (token, query head) pairs of up
+// to p.q_tokens rows of a sequence, whose remaining rows are further "sequences" of the stream; a
+// column sees the tokens up to its row's own.
+template <int D, int NT, bool kSmall, bool kRows>
 __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
     decode_e2m1_kernel(const DecodeParams p, const int HG, const bool small) {
     using C = ECfg<D, NT>;
@@ -129,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
     allow_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = lane >> 2, c = lane & 3;
-    const int G = p.group, Hkv = p.num_kv_heads, B = p.num_seqs, Bs = p.block_size;
+    const int G = p.group, Hkv = p.num_kv_heads, B = p.num_seqs, Bs = p.block_size, cols = p.cols;
     const int bs_shift = 31 - __clz(Bs);                    // block sizes are powers of two
     const int hl = warp % HG, groups = Hkv / HG;
     const int64_t slice = (int64_t)blockIdx.x * (kWarps / HG) + warp / HG;
@@ -138,12 +142,22 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
     // ---- the slice: lane i sums the slabs of sequences [i cs, (i + 1) cs), one scan joins them ----
     const int cs = (B + 31) / 32;
     const int c_lo = min(B, lane * cs), c_hi = min(B, c_lo + cs);
+    // tokens that sequence b's last column sees: its length, or with kRows that of its last row
+    auto length = [&](int32_t bb) -> int32_t {
+        if constexpr (kRows) {
+            int32_t row0, n;
+            return rows_length(p, bb, row0, n);
+        } else {
+            return clipped_length(p, bb);
+        }
+    };
+    auto table_row = [&](int32_t bb) { return (size_t)(kRows ? bb / p.q_chunks : bb) * p.max_blocks_per_seq; };
     auto slabs_of = [&](int32_t L) { return L == 0 ? 1 : (L + SL - 1) / SL; };
     int64_t lane_sum = 0, incl;
     if (small) {
         uint32_t sum = 0;
 #pragma unroll 4
-        for (int b = c_lo; b < c_hi; ++b) sum += slabs_of(clipped_length(p, b));
+        for (int b = c_lo; b < c_hi; ++b) sum += slabs_of(length(b));
         uint32_t acc = sum;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -153,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
         lane_sum = sum;
         incl = acc;
     } else {
-        for (int b = c_lo; b < c_hi; ++b) lane_sum += slabs_of(clipped_length(p, b));
+        for (int b = c_lo; b < c_hi; ++b) lane_sum += slabs_of(length(b));
         incl = lane_sum;
         for (int off = 1; off < 32; off <<= 1) {
             const int64_t v = __shfl_up_sync(0xffffffffu, incl, off);
@@ -175,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
         b = c_lo;
         int64_t acc = excl;
         if (lane == k) {
-            for (int n; rem >= acc + (n = slabs_of(clipped_length(p, b))); ++b) acc += n;
+            for (int n; rem >= acc + (n = slabs_of(length(b))); ++b) acc += n;
             j = (int32_t)(rem - acc);
             P = (int64_t)gi * S_seq + acc;
         }
@@ -185,9 +199,9 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
     }
 
     // ---- load cursor: the next slab to request, with its sequence's table window ----
-    int32_t L = clipped_length(p, b), nb = slabs_of(L);
+    int32_t L = length(b), nb = slabs_of(L);
     auto entry = [&](int32_t bb, int32_t idx) -> int32_t {
-        return idx < p.max_blocks_per_seq ? __ldg(p.block_tables + (size_t)bb * p.max_blocks_per_seq + idx) : -1;
+        return idx < p.max_blocks_per_seq ? __ldg(p.block_tables + table_row(bb) + idx) : -1;
     };
     int32_t win_base = (j * SL) >> bs_shift;
     int32_t win = entry(b, win_base + lane), win2 = entry(b, win_base + 32 + lane);
@@ -224,19 +238,19 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
                 win2 = entry(b, 32 + lane);
             }
             at_start = false;
-            if (lane < (G * D + 63) / 64)                   // its query rows, needed when it is processed
+            if (!kRows && lane < (G * D + 63) / 64)         // its query rows, needed when it is processed
                 asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + ((size_t)b * p.num_q_heads +
                                                                      (size_t)(gi * HG + hl) * G) * D + lane * 64));
             if (nb - j < left) {                            // the slice reaches the next sequence
                 const int32_t bn = b + 1 == B ? 0 : b + 1;
-                nx_len = __ldg(p.context_lens + bn);
+                nx_len = kRows ? length(bn) : __ldg(p.context_lens + bn);
                 nx_win = entry(bn, lane);
             }
         }
         const int32_t t0 = j * SL, kvh = gi * HG + hl;
         if (lane == 0) {
             const bool last = left == 1 || j == nb - 1;
-            slabs[st] = ESlab{b, kvh, min(SL, L - t0), (first ? kFirst : 0) | (last ? kLast : 0), P, nb};
+            slabs[st] = ESlab{b, kvh, L - t0, (first ? kFirst : 0) | (last ? kLast : 0), P, nb};
         }
         if (((t0 >> bs_shift) - win_base) >= 32) {          // a slab's blocks never straddle windows
             win_base += 32;
@@ -296,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
                 ++gi;
             }
             if (left > 0) {
-                L = clip_length(p, nx_len);
+                L = kRows ? nx_len : clip_length(p, nx_len);
                 nb = slabs_of(L);
             }
         }
@@ -309,16 +323,24 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
     float o_acc[NT][C::kSteps][4];
     const uint32_t sel = (r & 1) ? 0x3311u : 0x2200u;       // scales of tokens tau, tau + 2, each twice
 
+    int32_t fewer[NT][2], fewer_most = 0, row0 = 0, ntok = 1;   // kRows: tokens that a column sees fewer than the last
+
     auto start = [&](const ESlab& x) {
+        if constexpr (kRows) {
+            rows_length(p, x.b, row0, ntok);
+            fewer_most = ntok - 1;
+        } else {
+            row0 = x.b;
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int h = nt * 8 + r;
+            const int col = nt * 8 + r, tok = kRows ? col / G : 0, h = col - tok * G;
             uint4 qv[D / 32];
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) qv[i] = make_uint4(0, 0, 0, 0);
-            if (h < G) {
+            if (kRows ? tok < ntok : h < G) {
                 const uint4* src = reinterpret_cast<const uint4*>(
-                    p.q + ((size_t)x.b * p.num_q_heads + (size_t)x.kvh * G + h) * D + c * (D / 4));
+                    p.q + ((size_t)(row0 + tok) * p.num_q_heads + (size_t)x.kvh * G + h) * D + c * (D / 4));
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) qv[i] = __ldcg(src + i);
             }
@@ -343,7 +365,9 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
 #pragma unroll
             for (int jj = 0; jj < 2; ++jj) {
                 sl2[nt][jj] = __shfl_sync(0xffffffffu, back, (2 * c + jj) * 4);
-                m_run[nt][jj] = -INFINITY;
+                // finite, so that a slab with nothing for a column weighs nothing (and is no NaN)
+                m_run[nt][jj] = -FLT_MAX;
+                if (kRows) fewer[nt][jj] = max(0, ntok - 1 - (nt * 8 + 2 * c + jj) / G);
                 l_run[nt][jj] = 0.f;
             }
 #pragma unroll
@@ -376,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
         uint32_t stage_codes = ring + st * C::kStageBytes, stage_scales = stage_codes;
 
         if (x.valid == 0) {                                 // an empty sequence: zeros, nothing to join
-            store_zero_group(p, x.b, x.kvh, lane, 32);
+            if (!kRows) store_zero_group(p, x.b, x.kvh, lane, 32);   // kRows: there are no rows
             if (hl == 0 && lane == 0)
                 reinterpret_cast<int4*>(p.seq_desc)[(size_t)(x.kvh / HG) * B + x.b] = make_int4(1, 0, 0, 0);
             return;
@@ -392,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
                     make_int4(seg_split, i_first, x.P < slice_lo(i_first, S, Gc, small) ? 0 : 1, 0);
         }
 #pragma unroll 1
-        for (int valid = x.valid; valid > 0; valid -= 16 * CT, stage_codes += CT * kTileCodes, stage_scales += 2 * CT * C::kTileScales) {
+        for (int valid = x.valid, tile = 0; valid > 0 && tile < TS; valid -= 16 * CT, tile += CT, stage_codes += CT * kTileCodes, stage_scales += 2 * CT * C::kTileScales) {
         // ---- S = K q^T ----
         float sv[CT][NT][4];
 #pragma unroll
@@ -434,16 +458,15 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
         uint32_t vs4[CT];
 #pragma unroll
         for (int u = 0; u < CT; ++u) vs4[u] = lds32(stage_scales + vs_at + 2 * u * C::kTileScales);
-        if (valid < 16 * CT) {
+        if (valid - (kRows ? fewer_most : 0) < 16 * CT) {
             // tokens past the sequence: no weight; their V may hold any bytes, NaN scales among them
 #pragma unroll
             for (int u = 0; u < CT; ++u) {
-                const bool v_lo = 16 * u + tau < valid, v_hi = 16 * u + tau + 2 < valid;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (!(e < 2 ? v_lo : v_hi)) sv[u][nt][e] = -INFINITY;
+                        if (16 * u + tau + (e < 2 ? 0 : 2) >= valid - (kRows ? fewer[nt][e & 1] : 0)) sv[u][nt][e] = -INFINITY;
                 const int in = valid - 16 * u - v_quad;
                 if (in < 4) vs4[u] = in <= 0 ? 0u : vs4[u] & (0xFFFFFFFFu >> (32 - 8 * in));
             }
@@ -541,18 +564,18 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
                 for (int off = 4; off < 32; off <<= 1)
                     l_run[nt][jj] += __shfl_xor_sync(0xffffffffu, l_run[nt][jj], off);
         const bool whole = seg_split == 1;
-        const size_t prow = (((size_t)slice * 2 + seg_slot) * Hkv + x.kvh) * G;
+        const size_t prow = (((size_t)slice * 2 + seg_slot) * Hkv + x.kvh) * cols;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int jj = 0; jj < 2; ++jj) {
-                const int h = nt * 8 + 2 * c + jj;
-                if (h >= G) continue;
-                const float inv = p.out_scale / l_run[nt][jj];
+                const int col = nt * 8 + 2 * c + jj, tok = kRows ? col / G : 0, h = col - tok * G;
+                if (kRows ? tok >= ntok : h >= G) continue;
+                const float inv = l_run[nt][jj] == 0.f ? 0.f : p.out_scale / l_run[nt][jj];
                 // the lane's D / 8 dims r D / 8 ..: consecutive pairs
                 if (whole) {
                     uint4* out = reinterpret_cast<uint4*>(
-                        p.out + ((size_t)x.b * p.num_q_heads + (size_t)x.kvh * G + h) * D + r * (D / 8));
+                        p.out + ((size_t)(row0 + tok) * p.num_q_heads + (size_t)x.kvh * G + h) * D + r * (D / 8));
 #pragma unroll
                     for (int i = 0; i < W; ++i)
                         out[i] = make_uint4(
@@ -561,12 +584,13 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
                             pack_bf16x2(o_acc[nt][4 * i + 2][jj] * inv, o_acc[nt][4 * i + 2][jj + 2] * inv),
                             pack_bf16x2(o_acc[nt][4 * i + 3][jj] * inv, o_acc[nt][4 * i + 3][jj + 2] * inv));
                 } else {
-                    float4* po = reinterpret_cast<float4*>(p.part_o + (prow + h) * D + r * (D / 8));
+                    float4* po = reinterpret_cast<float4*>(p.part_o + (prow + col) * D + r * (D / 8));
 #pragma unroll
                     for (int i = 0; i < 2 * W; ++i)
                         po[i] = make_float4(o_acc[nt][2 * i][jj] * inv, o_acc[nt][2 * i][jj + 2] * inv,
                                             o_acc[nt][2 * i + 1][jj] * inv, o_acc[nt][2 * i + 1][jj + 2] * inv);
-                    if (r == 0) p.part_lse[prow + h] = m_run[nt][jj] + __log2f(l_run[nt][jj]);
+                    if (r == 0)
+                        p.part_lse[prow + col] = l_run[nt][jj] == 0.f ? -FLT_MAX : m_run[nt][jj] + __log2f(l_run[nt][jj]);
                 }
             }
     };
@@ -590,14 +614,14 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
     }
 }
 
-template <int D, int NT, bool kSmall>
+template <int D, int NT, bool kSmall, bool kRows>
 bool ensure_smem() {
     static std::atomic<uint64_t> done{0};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
     const uint64_t bit = 1ull << dev;
     if (done.load(std::memory_order_acquire) & bit) return true;
-    if (cudaFuncSetAttribute(decode_e2m1_kernel<D, NT, kSmall>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(decode_e2m1_kernel<D, NT, kSmall, kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)ECfg<D, NT>::kSmem) != cudaSuccess)
         return false;
     done.fetch_or(bit, std::memory_order_acq_rel);
@@ -611,19 +635,17 @@ int occupancy() {
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
     int occ = cache[dev].load(std::memory_order_acquire);
     if (occ > 0) return occ;
-    if (!ensure_smem<D, NT, false>() ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, decode_e2m1_kernel<D, NT, false>, kThreads,
+    if (!ensure_smem<D, NT, false, false>() ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, decode_e2m1_kernel<D, NT, false, false>, kThreads,
                                                       ECfg<D, NT>::kSmem) != cudaSuccess)
         return 0;
     cache[dev].store(occ, std::memory_order_release);
     return occ;
 }
 
-template <int D, int NT>
-cudaError_t launch_e(const DecodeParams& p, int grid, bool pdl, cudaStream_t stream) {
-    const bool small = p.block_size < 16;
-    if (!(small ? ensure_smem<D, NT, true>() : ensure_smem<D, NT, false>())) return cudaErrorInvalidConfiguration;
-    const auto kernel = small ? decode_e2m1_kernel<D, NT, true> : decode_e2m1_kernel<D, NT, false>;
+template <int D, int NT, bool kSmall, bool kRows>
+cudaError_t launch_k(const DecodeParams& p, int grid, bool pdl, cudaStream_t stream) {
+    if (!ensure_smem<D, NT, kSmall, kRows>()) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kThreads);
@@ -638,7 +660,16 @@ cudaError_t launch_e(const DecodeParams& p, int grid, bool pdl, cudaStream_t str
     const uint64_t slabs = (uint64_t)p.num_seqs * (p.num_kv_heads / p.desc_heads) *
                            ((uint64_t)p.max_context_len / ECfg<D, NT>::kSlab + 1);
     const bool fits = (slabs + 1) * ((uint64_t)p.grid + 1) < (1ull << 32);
-    return cudaLaunchKernelEx(&cfg, kernel, p, p.desc_heads, fits);
+    return cudaLaunchKernelEx(&cfg, decode_e2m1_kernel<D, NT, kSmall, kRows>, p, p.desc_heads, fits);
+}
+
+template <int D, int NT>
+cudaError_t launch_e(const DecodeParams& p, int grid, bool pdl, cudaStream_t stream) {
+    const bool small = p.block_size < 16;
+    if (p.cu_q) return small ? launch_k<D, NT, true, true>(p, grid, pdl, stream)
+                             : launch_k<D, NT, false, true>(p, grid, pdl, stream);
+    return small ? launch_k<D, NT, true, false>(p, grid, pdl, stream)
+                 : launch_k<D, NT, false, false>(p, grid, pdl, stream);
 }
 
 }  // namespace
@@ -650,10 +681,10 @@ int e2m1_head_group(int num_kv_heads) {
 }
 int e2m1_slab_tokens(int head_dim) { return head_dim == 64 ? ECfg<64, 1>::kSlab : ECfg<128, 1>::kSlab; }
 
-int e2m1_kernel_grid(const pa_cache_desc& d, int max_ctas) {
+int e2m1_kernel_grid(const pa_cache_desc& d, int cols, int max_ctas) {
     int sms = 0;
     if (num_sms_current_device(&sms) != PA_OK) return 0;
-    const bool two = d.num_q_heads / d.num_kv_heads > 8;
+    const bool two = cols > 8;
     const int occ = d.head_dim == 64 ? (two ? occupancy<64, 2>() : occupancy<64, 1>())
                                      : (two ? occupancy<128, 2>() : occupancy<128, 1>());
     if (occ <= 0) return 0;
@@ -662,7 +693,7 @@ int e2m1_kernel_grid(const pa_cache_desc& d, int max_ctas) {
 }
 
 cudaError_t launch_decode_e2m1(const DecodeParams& p, int grid, bool pdl, cudaStream_t stream) {
-    const bool two = p.group > 8;
+    const bool two = p.cols > 8;
     if (p.head_dim == 64)
         return two ? launch_e<64, 2>(p, grid, pdl, stream) : launch_e<64, 1>(p, grid, pdl, stream);
     if (p.head_dim == 128)

@@ -27,6 +27,17 @@ namespace {
 // sequence into many pieces: 16 groups keep each thread's chain short there.
 // kStream: the stream partition's pieces (read from the sequence's descriptor);
 // else the split kernels' fixed splits.
+// Output row of column h (of p.cols) of kv head kvh: query head h of sequence b, or with few-row
+// prefill the (token, head) pair of it; -1 for a token that the sequence does not have.
+__device__ __forceinline__ int64_t merge_out_row(const DecodeParams& p, int32_t b, int32_t kvh, int32_t h) {
+    if (!p.cu_q) return (int64_t)b * p.num_q_heads + (int64_t)kvh * p.group + h;
+    int32_t row0, ntok;
+    if (rows_length(p, b, row0, ntok) == 0) return -1;
+    const int32_t tok = h / p.group;
+    if (tok >= ntok) return -1;
+    return (int64_t)(row0 + tok) * p.num_q_heads + (int64_t)kvh * p.group + (h - tok * p.group);
+}
+
 template <int D, bool kStream, int PG>
 __global__ void __launch_bounds__(PG * D / 4) merge_kernel(const DecodeParams p) {
     constexpr int kCols = D / 4;
@@ -36,7 +47,7 @@ __global__ void __launch_bounds__(PG * D / 4) merge_kernel(const DecodeParams p)
     __shared__ float4 s_acc[kPieceGroups][kCols];
     __shared__ float s_m[kPieceGroups], s_w[kPieceGroups];
     const int32_t b = blockIdx.x, kvh = blockIdx.y, h = blockIdx.z;
-    const int32_t G = p.group, Hkv = p.num_kv_heads;
+    const int32_t G = p.cols, Hkv = p.num_kv_heads;
     const int tid = threadIdx.x;
     int32_t nsplit;
     size_t first_row, row0, row_step;   // piece 0: first_row; piece k >= 1: row0 + (k-1) * row_step
@@ -102,7 +113,8 @@ __global__ void __launch_bounds__(PG * D / 4) merge_kernel(const DecodeParams p)
         uint2 packed;
         packed.x = pack_bf16x2(t.x * inv, t.y * inv);
         packed.y = pack_bf16x2(t.z * inv, t.w * inv);
-        reinterpret_cast<uint2*>(p.out + ((size_t)b * p.num_q_heads + (size_t)kvh * G + h) * D)[tid] = packed;
+        const int64_t row = merge_out_row(p, b, kvh, h);
+        if (row >= 0) reinterpret_cast<uint2*>(p.out + row * D)[tid] = packed;
     }
 }
 
@@ -116,7 +128,7 @@ __global__ void __launch_bounds__(1024) merge_stream_kernel(const DecodeParams p
     allow_dependents();   // a next decode call launched early may plan while this runs
     wait_prerequisite();
     extern __shared__ float4 s_dyn[];
-    const int32_t b = blockIdx.x, kvh = blockIdx.y, G = p.group, Hkv = p.num_kv_heads;
+    const int32_t b = blockIdx.x, kvh = blockIdx.y, G = p.cols, Hkv = p.num_kv_heads;
     const int4 dsc = reinterpret_cast<const int4*>(p.seq_desc)[(size_t)(kvh / p.desc_heads) * p.num_seqs + b];
     const int32_t nsplit = dsc.x;
     if (nsplit <= 1) return;
@@ -168,14 +180,15 @@ __global__ void __launch_bounds__(1024) merge_stream_kernel(const DecodeParams p
     uint2 packed;
     packed.x = pack_bf16x2(tot.x * inv, tot.y * inv);
     packed.y = pack_bf16x2(tot.z * inv, tot.w * inv);
-    reinterpret_cast<uint2*>(p.out + ((size_t)b * p.num_q_heads + (size_t)kvh * G + h) * D)[col] = packed;
+    const int64_t row = merge_out_row(p, b, kvh, h);
+    if (row >= 0) reinterpret_cast<uint2*>(p.out + row * D)[col] = packed;
 }
 
 template <int D>
 cudaError_t launch_ms(const DecodeParams& p, bool pdl, cudaStream_t stream) {
     int sms = 0;
     if (num_sms_current_device(&sms) != PA_OK) return cudaErrorInvalidDevice;
-    const int C = p.group * (D / 4);
+    const int C = p.cols * (D / 4);
     const int64_t ctas = (int64_t)p.num_seqs * p.num_kv_heads;
     const int64_t per_cta = (int64_t)sms * 2048 / (ctas * C);   // threads per column for one wave
     int PG = 1;
@@ -183,7 +196,7 @@ cudaError_t launch_ms(const DecodeParams& p, bool pdl, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)p.num_seqs, (unsigned)p.num_kv_heads);
     cfg.blockDim = dim3((unsigned)(PG * C));
-    cfg.dynamicSmemBytes = (size_t)PG * C * sizeof(float4) + (size_t)PG * p.group * sizeof(float2);
+    cfg.dynamicSmemBytes = (size_t)PG * C * sizeof(float4) + (size_t)PG * p.cols * sizeof(float2);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -196,7 +209,7 @@ cudaError_t launch_ms(const DecodeParams& p, bool pdl, cudaStream_t stream) {
 template <int D, bool kStream, int PG>
 cudaError_t launch_m(const DecodeParams& p, bool pdl, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.num_seqs, (unsigned)p.num_kv_heads, (unsigned)p.group);
+    cfg.gridDim = dim3((unsigned)p.num_seqs, (unsigned)p.num_kv_heads, (unsigned)p.cols);
     cfg.blockDim = dim3(PG * D / 4);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -222,7 +235,7 @@ template <int D>
 cudaError_t launch_stream_merge(const DecodeParams& p, bool pdl, cudaStream_t stream) {
     int sms = 0;
     if (num_sms_current_device(&sms) != PA_OK) return cudaErrorInvalidDevice;
-    const int64_t per_head_ctas = (int64_t)p.num_seqs * p.num_kv_heads * p.group;
+    const int64_t per_head_ctas = (int64_t)p.num_seqs * p.num_kv_heads * p.cols;
     if (per_head_ctas <= (int64_t)sms * 16) return launch_mg<D, true>(p, pdl, stream);
     return launch_ms<D>(p, pdl, stream);
 }

@@ -64,6 +64,22 @@ __device__ __forceinline__ int32_t clipped_length(const DecodeParams& p, int32_t
     return clip_length(p, p.context_lens[b]);
 }
 
+// Few-row prefill: "sequence" v is chunk v % q_chunks of sequence v / q_chunks.  Its first row (of q and
+// out), its number of rows, and the tokens that its last row sees; 0 for a chunk without rows, or of a
+// sequence whose lengths cannot hold its rows (reported).
+__device__ __forceinline__ int32_t rows_length(const DecodeParams& p, int32_t v, int32_t& row0, int32_t& n) {
+    const int32_t b = v / p.q_chunks, first = (v - b * p.q_chunks) * p.q_tokens;
+    const int32_t q0 = p.cu_q[b], Tq = p.cu_q[b + 1] - q0, L = p.context_lens[b];
+    row0 = q0 + first;
+    n = min(p.q_tokens, Tq - first);
+    if (n <= 0) return 0;
+    if (L < Tq || (int64_t)L > (int64_t)p.max_blocks_per_seq * p.block_size || L > p.max_context_len || Tq > p.max_q_len) {
+        raise_status(p.status, kStatusBadLength);
+        return 0;
+    }
+    return L - Tq + first + n;
+}
+
 // RoPE: pair i (of D/2) at position pos turns by a = pos * theta^(-2i/D).  The
 // inverse frequency theta^(-2i/D) is formed once per CTA in double; the angle
 // is formed and reduced to [-pi, pi] in double (positions reach 2^17, where a

@@ -53,6 +53,11 @@ struct DecodeParams {
     int32_t grid;                  // stream kernels: slices of the launch (bounds the merge's reads)
     int32_t desc_heads;            // stream kernels: kv heads that share one seq_desc row
 
+    int32_t cols;                  // columns a kv head: the group, or few-row prefill's (token, head) pairs
+    const int32_t* cu_q;           // few-row prefill: row offsets [B + 1] (num_seqs = B * q_chunks), or null
+    int32_t q_tokens, q_chunks;    // few-row prefill: rows a chunk of a sequence, chunks a sequence at most
+    int32_t max_q_len;
+
     int32_t selftest_stall;        // PA_FLAG_SELFTEST_STALL: CTA 0 of the stream kernel idles
     unsigned long long wait_ns;    // limit of every bounded wait in the stream kernel
 };
@@ -137,7 +142,7 @@ cudaError_t launch_decode_e2m1(const DecodeParams& p, int grid, bool pdl, cudaSt
 cudaError_t launch_prefill_e2m1(const PrefillParams& p, int max_q_len, cudaStream_t stream);
 int e2m1_head_group(int num_kv_heads);
 int e2m1_slab_tokens(int head_dim);
-int e2m1_kernel_grid(const pa_cache_desc& d, int max_ctas);
+int e2m1_kernel_grid(const pa_cache_desc& d, int cols, int max_ctas);
 // RoPE + append through the slot mapping (pa_rope_append_kv).
 cudaError_t launch_rope_append(const pa_bf16* q, pa_bf16* q_out, const pa_bf16* k, const pa_bf16* v,
                                const int32_t* positions, const int64_t* slots, int32_t T, float theta,
