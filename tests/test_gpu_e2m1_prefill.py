@@ -29,7 +29,7 @@ def test_refusals():
                                          ws, size, ctypes.byref(d), ctypes.byref(o), None)
 
     for bad in (dict(k_scale=0.0), dict(v_scale=-1.0), dict(k_scale=float("nan")), dict(v_scale=1e-39),
-                dict(kv_dtype=9), dict(kernel=4), dict(kernel=-1), dict(n=-1), dict(rows=-1), dict(longest=-1),
+                dict(kv_dtype=9), dict(kernel=5), dict(kernel=-1), dict(n=-1), dict(rows=-1), dict(longest=-1),
                 dict(scale=0.0), dict(scale=float("inf")), dict(q=None), dict(q=mis), dict(d=_desc(num_q_heads=5))):
         assert call(**bad) == -1, bad
     for bad in (dict(kv_dtype=pa.PA_KV_E4M3), dict(kernel=pa.PA_PREFILL_MMA), dict(kernel=pa.PA_PREFILL_TCGEN05),
