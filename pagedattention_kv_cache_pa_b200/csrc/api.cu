@@ -792,7 +792,7 @@ extern "C" int pa_cross_attention(const pa_bf16* q, const pa_bf16* k_cache, cons
         return PA_ERR_WORKSPACE;
     const PrefillParams p = prefill_params(q, k_cache, v_cache, block_tables, cu_seqlens_q, encoder_lens, num_seqs,
                                            max_q_len, scale, out, workspace, *desc);
-    const cudaError_t e = launch_cross_ws(p, max_q_len, (cudaStream_t)stream);
+    const cudaError_t e = launch_cross(p, max_q_len, (cudaStream_t)stream);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

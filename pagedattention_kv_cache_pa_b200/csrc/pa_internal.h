@@ -103,6 +103,7 @@ cudaError_t launch_prefill_tc(const PrefillParams& p, int max_q_len, cudaStream_
 cudaError_t launch_prefill_ws(const PrefillParams& p, int max_q_len, cudaStream_t stream);
 // the same tiles without the causal mask (cross attention)
 cudaError_t launch_cross_ws(const PrefillParams& p, int max_q_len, cudaStream_t stream);
+cudaError_t launch_cross(const PrefillParams& p, int max_q_len, cudaStream_t stream);
 bool prefill_ws_supports(int block_size);
 
 constexpr size_t kWorkspaceAlign = 256;
