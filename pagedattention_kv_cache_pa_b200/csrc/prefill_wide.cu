@@ -8,7 +8,7 @@
 //  * An MMA of 128 x 64 x 16 takes as long as one of 128 x 128 x 16: the A operand is read from
 //    shared memory either way (16 of the first: 1013 cycles, of the second: 1139).  So tiles hold 128
 //    keys.  For S and P of 128 keys and O of 128 dims, of two row tiles, tensor memory is exactly
-//    enough when P takes the place of S.
+//    enough when P takes the place of S (with 64 dims P has columns of its own).
 //  * Issued by one thread of a divergent warp, whose descriptors go through vector registers, the
 //    MMAs of a 64-dim head cost 80 cycles each; issued by an elected lane of a warp that runs as a
 //    whole, 43 (ideal 32).  So the MMA warp runs as a whole.
@@ -19,7 +19,7 @@
 // taken in zigzag as in prefill_ws.cu.  Warps with one job each meet through mbarriers only:
 //   warps 0-3, 4-7  softmax of row tile 0 and 1: thread = row.  S out of tensor memory (64 keys at a
 //                   time; those of the first half twice, to hold no more), the mask, the running max
-//                   with lazy rescale of O in tensor memory, P back over the second half of S.
+//                   with lazy rescale of O in tensor memory, P back.
 //   warps 8-11      K and V tiles.  4-bit: thread = key; codes and scales of the next tile are in
 //                   flight in registers while this one is widened, V to f16 (one conversion and one
 //                   product a pair, exact), K to bf16, q's type (the f16 pattern of a code shifted
@@ -27,7 +27,7 @@
 //                   exact too).  bf16: warp 8 requests TMA boxes of 64 dims x min(Bs, 64) tokens.
 //                   Rows of V past the sequence are zero, so P = 0 never meets a NaN there.
 //   warp 12         (of a fourth warpgroup) MMA issue: O += P(t) V(t) of a row tile, then its
-//                   S(t + 1), which may overwrite P(t) as MMAs run in order.  While one row tile's
+//                   S(t + 1), which with 128 dims overwrites P(t): MMAs of one shape run in order.  While one row tile's
 //                   products run, the other's softmax has the exponential unit to itself.
 // K and V tiles have rings of their own.
 //
@@ -75,7 +75,9 @@ struct PCfg {
     // k_empty, v_full, v_empty
     static constexpr int kBars = 14 + 4 * kStages;
     static constexpr int kSmem = kOffBar + kBars * 8 + 16;
-    static constexpr int kColS = 0, kColP = 64, kColO = 256;       // S: 128 a group, P in its second half; O: D
+    // S: 128 columns a group; P: over the second half of S where O leaves no room for columns of its own
+    static constexpr bool kOverS = D == 128;
+    static constexpr int kColS = 0, kColP = kOverS ? 64 : 256, kStepP = kOverS ? 128 : 64, kColO = kOverS ? 256 : 384;
     static constexpr uint32_t kTmemCols = 512;
     static_assert(kColO + 2 * D <= 512 && kSmem <= 227 * 1024, "tensor and shared memory of one CTA");
 };
@@ -475,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (leader) {
 #pragma unroll
                     for (int k = 0; k < kKeys / 16; ++k)
-                        umma_bf16_ts(tmem + C::kColO + gr * D, tmem + C::kColS + gr * kKeys + C::kColP + k * 8,
+                        umma_bf16_ts(tmem + C::kColO + gr * D, tmem + C::kColP + gr * C::kStepP + k * 8,
                                      umma_desc_sw128(vt + k * 16 * 128, kKeys * 128, 1024), kIdescO,
                                      (!first || k > 0) ? 1u : 0u);
                     umma_commit(bar_o(gr));
@@ -540,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ============================== softmax ==============================
         const int gr = warp >> 2, tr = tid & (kRows - 1);    // row tile, row in it
         const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t t_s = t_lane + C::kColS + gr * kKeys, t_p = t_s + C::kColP, t_o = t_lane + C::kColO + gr * D;
+        const uint32_t t_s = t_lane + C::kColS + gr * kKeys, t_p = t_lane + C::kColP + gr * C::kStepP, t_o = t_lane + C::kColO + gr * D;
         const float sl2 = p.scale_log2;
         auto wait_o = [&](int tt) { return warp_wait(bar_o(gr), (uint32_t)(tt & 1), p.status); };
         constexpr int kRowStep = kRows / kCh;
@@ -669,8 +671,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         rs2[j & 1] = f2_add(rs2[j & 1], f2(p0, p1));
                         pk[j] = pack_p<kE2m1>(p0, p1);
                     }
+                    // P's own columns: once the products of the previous tile have read them
+                    if (!C::kOverS && half == 1 && t > 0 && !wait_o(tt - 1)) {
+                        failed = true;
+                        break;
+                    }
                     tmem_st32(t_p + half * 32, pk);
                 }
+                if (failed) break;
                 float r0a, r0b, r1a, r1b;
                 f2_split(rs2[0], r0a, r0b);
                 f2_split(rs2[1], r1a, r1b);
