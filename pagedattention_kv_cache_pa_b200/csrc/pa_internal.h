@@ -101,7 +101,7 @@ cudaError_t launch_prefill(const PrefillParams& p, int max_q_len, cudaStream_t s
 cudaError_t launch_prefill_tc(const PrefillParams& p, int max_q_len, cudaStream_t stream);
 // warp-specialized tcgen05 prefill (TMA block sizes only: 8, 16, 32, 64 or multiples of 64)
 cudaError_t launch_prefill_ws(const PrefillParams& p, int max_q_len, cudaStream_t stream);
-// the same tiles without the causal mask (cross attention)
+// cross attention: either kernel's tiles without the causal mask
 cudaError_t launch_cross_ws(const PrefillParams& p, int max_q_len, cudaStream_t stream);
 cudaError_t launch_cross(const PrefillParams& p, int max_q_len, cudaStream_t stream);
 bool prefill_ws_supports(int block_size);

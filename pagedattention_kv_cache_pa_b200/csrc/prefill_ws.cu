@@ -651,9 +651,8 @@ cudaError_t launch_prefill_ws(const PrefillParams& p, int max_q_len, cudaStream_
 }
 
 cudaError_t launch_cross_ws(const PrefillParams& p, int max_q_len, cudaStream_t stream) {
-    if (p.head_dim == 64) return launch_ws<64, false>(p, max_q_len, stream);
-    if (p.head_dim == 128) return launch_ws<128, false>(p, max_q_len, stream);
-    return cudaErrorInvalidValue;
+    // 128 dims: prefill_wide.cu
+    return p.head_dim == 64 ? launch_ws<64, false>(p, max_q_len, stream) : cudaErrorInvalidValue;
 }
 
 }  // namespace pa
