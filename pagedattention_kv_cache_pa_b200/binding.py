@@ -233,7 +233,19 @@ def _cache(t, desc: "CacheDesc", what: str, options=None):
             need = need * 9 // 16
         if t.numel() < need:
             raise ValueError("%s holds %d elements, the pool described needs %d" % (what, t.numel(), need))
-    return _dev(t, "bfloat16" if kv_dtype == PA_KV_BF16 else "uint8", what)
+    ptr = _dev(t, "bfloat16" if kv_dtype == PA_KV_BF16 else "uint8", what)
+    if kv_dtype == PA_KV_E2M1:
+        _on_current_device(t, what)
+    return ptr
+
+
+def _on_current_device(t, what: str) -> None:
+    """The kernels run on the current device's stream: refuse a tensor of another one."""
+    if t is None or isinstance(t, int):
+        return
+    import torch
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError("%s is on %s, the current device is cuda:%d" % (what, t.device, torch.cuda.current_device()))
 
 
 def _rows(t, num_tokens: int, heads: int, desc: "CacheDesc", what: str):
@@ -428,6 +440,7 @@ def pa_cross_attention(q, k_cache, v_cache, block_tables, cu_seqlens_q, encoder_
 
     cu_seqlens_q: int32 [num_seqs + 1] row offsets, or None for one row a sequence (max_q_len 1)."""
     n = int(encoder_lens.shape[0])
+    _on_current_device(k_cache, "k_cache")
     _check(lib.pa_cross_attention(_dev(q, "bfloat16", "q"), _cache(k_cache, desc, "k_cache"),
                                   _cache(v_cache, desc, "v_cache"), _dev(block_tables, "int32", "block_tables"),
                                   _dev(cu_seqlens_q, "int32", "cu_seqlens_q"),

@@ -24,7 +24,7 @@
 //
 // The work is the concatenation, over groups of HG kv heads (HG = 8, 4, 2 or 1, the largest that
 // divides Hkv) and sequences, of slabs of tokens (an empty sequence counts one).  8 / HG teams of
-// HG warps a CTA take equal slices of it; a team's warps read the same tokens, one kv head each, so
+// HG warps a TSA take equal slices of it; a team's warps read the same tokens, one kv head each, so
 // that the team reads a page's heads together.  A sequence that lies in one slice is written out;
 // one cut between slices leaves fp32 partial states, two a slice at most, which the merge kernel
 // (merge.cu) joins.
@@ -50,7 +50,6 @@ struct ECfg {
     static constexpr int kTiles = D == 64 ? 4 : 2;          // 16-token tiles a slab
     static constexpr int kSlab = 16 * kTiles;
     static constexpr int kStages = 3;                       // slabs of a warp's ring
-    static constexpr int kChunk = D == 64 ? 2 : 1;          // tiles processed at a time (the code of one turn)
     static constexpr int kW = D / 64;                       // words of 8 codes a lane and token (V); half of K's
     static constexpr int kSteps = D / 16;                   // k steps of S, m tiles of O
     static constexpr int kMinBlocks = NT == 1 ? 2 : 1;
@@ -382,13 +381,13 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
     const int k_quad = 4 * (r >> 1), v_quad = 4 * c;        // first token of the scale words
     uint32_t k_at[2], v_at[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2; ++i)   // (D = 128: two tokens on is the next line, under the same permutation)
         k_at[i] = D == 64 ? code_chunk<D>((tau + 2 * i) * 2 + (c >> 1)) * 16 + (c & 1) * 8
-                          : code_chunk<D>((tau + 2 * i) * 4 + c) * 16;
+                          : code_chunk<D>(tau * 4 + c) * 16 + 128 * i;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         v_at[i] = C::kCodeBytes + (D == 64 ? code_chunk<D>((v_quad + i) * 2 + (r >> 2)) * 16 + (r & 3) * 4
-                                           : code_chunk<D>((v_quad + i) * 4 + (r >> 1)) * 16 + (r & 1) * 8);
+                                           : code_chunk<D>((v_quad + (i & 1)) * 4 + (r >> 1)) * 16 + (r & 1) * 8 + 128 * (i >> 1));
     // scales of group g, four tokens from `quad`: [g][16 tokens], or [page][g][8 tokens]
     auto scale_at = [&](int g, int quad) {
         return 2 * C::kCodeBytes + (kSmall ? (quad >> 3) * (D / 2) + g * 8 + (quad & 7) : g * 16 + quad);
@@ -396,8 +395,8 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
     const uint32_t ks_at = scale_at(c * W, k_quad), vs_at = scale_at(D == 64 ? r >> 1 : r, v_quad) + C::kTileScales;
 
     auto process = [&](const ESlab& x, int st) {
-        constexpr int CT = C::kChunk;
-        uint32_t stage_codes = ring + st * C::kStageBytes, stage_scales = stage_codes;
+        const uint32_t stage = ring + st * C::kStageBytes;
+        const int valid = x.valid;
 
         if (x.valid == 0) {                                 // an empty sequence: zeros, nothing to join
             if (!kRows) store_zero_group(p, x.b, x.kvh, lane, 32);   // kRows: there are no rows
@@ -415,26 +414,24 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
                 reinterpret_cast<int4*>(p.seq_desc)[(size_t)(x.kvh / HG) * B + x.b] =
                     make_int4(seg_split, i_first, x.P < slice_lo(i_first, S, Gc, small) ? 0 : 1, 0);
         }
-#pragma unroll 1
-        for (int valid = x.valid, tile = 0; valid > 0 && tile < TS; valid -= 16 * CT, tile += CT, stage_codes += CT * kTileCodes, stage_scales += 2 * CT * C::kTileScales) {
         // ---- S = K q^T ----
-        float sv[CT][NT][4];
+        float sv[TS][NT][4];
 #pragma unroll
-        for (int u = 0; u < CT; ++u) {
+        for (int u = 0; u < TS; ++u) {
             uint32_t kw[2][2 * W];                          // codes of tokens tau, tau + 2
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 if constexpr (D == 64) {
-                    const uint2 a = lds64(stage_codes + k_at[h] + u * kTileCodes);
+                    const uint2 a = lds64(stage + k_at[h] + u * kTileCodes);
                     kw[h][0] = a.x; kw[h][1] = a.y;
                 } else {
-                    const uint4 a = lds128(stage_codes + k_at[h] + u * kTileCodes);
+                    const uint4 a = lds128(stage + k_at[h] + u * kTileCodes);
                     kw[h][0] = a.x; kw[h][1] = a.y; kw[h][2] = a.z; kw[h][3] = a.w;
                 }
             }
 #pragma unroll
             for (int i = 0; i < W; ++i) {                   // one scale group: 16 dims, 4 k steps
-                const uint32_t ss = __byte_perm(lds32(stage_scales + ks_at + 2 * u * C::kTileScales + i * (kSmall ? 8 : 16)), 0u, sel);
+                const uint32_t ss = __byte_perm(lds32(stage + ks_at + 2 * u * C::kTileScales + i * (kSmall ? 8 : 16)), 0u, sel);
                 const uint32_t s0 = e4m3x2_to_f16x2(ss), s1 = e4m3x2_to_f16x2(ss >> 16);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
@@ -455,13 +452,13 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
             }
         }
         // ---- online softmax in the log2 domain, the running max kept lazily ----
-        uint32_t vs4[CT];
+        uint32_t vs4[TS];
 #pragma unroll
-        for (int u = 0; u < CT; ++u) vs4[u] = lds32(stage_scales + vs_at + 2 * u * C::kTileScales);
-        if (valid - (kRows ? fewer_most : 0) < 16 * CT) {
+        for (int u = 0; u < TS; ++u) vs4[u] = lds32(stage + vs_at + 2 * u * C::kTileScales);
+        if (valid - (kRows ? fewer_most : 0) < 16 * TS) {
             // tokens past the sequence: no weight; their V may hold any bytes, NaN scales among them
 #pragma unroll
-            for (int u = 0; u < CT; ++u) {
+            for (int u = 0; u < TS; ++u) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -478,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
             mx[nt][0] = fmaxf(sv[0][nt][0], sv[0][nt][2]);
             mx[nt][1] = fmaxf(sv[0][nt][1], sv[0][nt][3]);
 #pragma unroll
-            for (int u = 1; u < CT; ++u) {
+            for (int u = 1; u < TS; ++u) {
                 mx[nt][0] = fmax3(mx[nt][0], sv[u][nt][0], sv[u][nt][2]);
                 mx[nt][1] = fmax3(mx[nt][1], sv[u][nt][1], sv[u][nt][3]);
             }
@@ -506,9 +503,9 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
                     }
                 }
         }
-        uint32_t pb[CT][NT][2];
+        uint32_t pb[TS][NT][2];
 #pragma unroll
-        for (int u = 0; u < CT; ++u)
+        for (int u = 0; u < TS; ++u)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const float p0 = fast_exp2(fmaf(sv[u][nt][0], sl2[nt][0], -m_run[nt][0]));
@@ -522,15 +519,15 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
             }
         // ---- O^T += V^T P ----
 #pragma unroll
-        for (int u = 0; u < CT; ++u) {
+        for (int u = 0; u < TS; ++u) {
             const uint32_t vs = vs4[u];
             uint32_t vw[4][W];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 if constexpr (D == 64) {
-                    vw[t][0] = lds32(stage_codes + v_at[t] + u * kTileCodes);
+                    vw[t][0] = lds32(stage + v_at[t] + u * kTileCodes);
                 } else {
-                    const uint2 a = lds64(stage_codes + v_at[t] + u * kTileCodes);
+                    const uint2 a = lds64(stage + v_at[t] + u * kTileCodes);
                     vw[t][0] = a.x; vw[t][1] = a.y;
                 }
             }
@@ -552,7 +549,6 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
                     for (int nt = 0; nt < NT; ++nt) mma_f16_16816(o_acc[nt][4 * i + k], a, pb[u][nt][0], pb[u][nt][1]);
                 }
             }
-        }
         }
         if (!(x.flags & kLast)) return;
         // ---- end of the segment: write out, or leave a partial state ----
@@ -597,19 +593,20 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
 
     // everything below reads or writes what the previous kernel on the stream may touch
     wait_prerequisite();
+    // slab i is requested kStages - 1 turns before it is processed (one copy of the code for both)
     const int32_t todo = left;
-#pragma unroll
-    for (int i = 0; i < C::kStages - 1; ++i) {
-        if (left > 0) fetch(i);
+    for (int32_t i = 1 - C::kStages, st = 1, ahead = 0; i < todo; ++i) {
+        if (i >= 0) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
+            __syncwarp();                                   // every lane's copies of slab i; slab i - 1 read by all
+        }
+        if (left > 0) fetch(ahead);
         asm volatile("cp.async.commit_group;" ::: "memory");
-    }
-    for (int32_t i = 0, st = 0; i < todo; ++i) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
-        __syncwarp();                                       // every lane's copies of slab i; slab i - 1 read by all
-        if (left > 0) fetch(st == 0 ? C::kStages - 1 : st - 1);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        const ESlab x = slabs[st];
-        process(x, st);
+        ahead = ahead + 1 == C::kStages ? 0 : ahead + 1;
+        if (i >= 0) {
+            const ESlab x = slabs[st];
+            process(x, st);
+        }
         st = st + 1 == C::kStages ? 0 : st + 1;
     }
 }

@@ -276,6 +276,13 @@ def test_decode_q_of_any_size(h, q_scale):
     c.check(h)
 
 
+@pytest.mark.parametrize("scale", [-0.25, 0.0, -1e-3])
+def test_decode_scale_of_any_sign(h, scale):
+    c = Case(23, [200, 77, 1], 16, 4, 64, 16, q_scale=2.0)
+    c.scale = scale
+    c.check(h)
+
+
 def test_decode_rising_and_far_scores(h):
     # K rows that grow along the sequence raise the running max at every slab; others fall far below it
     c = Case(31, [640], 8, 8, 64, 16, q_scale=4.0)
