@@ -228,32 +228,47 @@ def _cache(t, desc: "CacheDesc", what: str, options=None):
     options say so) that holds at least the pool desc describes."""
     kv_dtype = PA_KV_BF16 if options is None else options.kv_dtype
     if t is not None and not isinstance(t, int):
-        need = desc.num_blocks * desc.num_kv_heads * desc.block_size * desc.head_dim
-        if kv_dtype == PA_KV_E2M1:
-            need = need * 9 // 16
+        need = _pool_elements(desc, kv_dtype)
         if t.numel() < need:
             raise ValueError("%s holds %d elements, the pool described needs %d" % (what, t.numel(), need))
-    ptr = _dev(t, "bfloat16" if kv_dtype == PA_KV_BF16 else "uint8", what)
     if kv_dtype == PA_KV_E2M1:
-        _on_current_device(t, what)
+        return _here(t, "uint8", what, _device())
+    return _dev(t, "bfloat16" if kv_dtype == PA_KV_BF16 else "uint8", what)
+
+
+def _here(t, dtype_name: str, what: str, device: int, need: int = 0):
+    """Device pointer of a contiguous tensor (or a raw int) of at least `need` elements on `device`, the
+    current one: the kernels run on its stream, so tensors of another are refused."""
+    if t is None or isinstance(t, int):
+        return t
+    if (t.dtype is _DTYPES.get(dtype_name) and t.get_device() == device and t.is_contiguous()
+            and t.numel() >= need):
+        return t.data_ptr()
+    ptr = _dev(t, dtype_name, what)
+    if t.get_device() != device:
+        raise ValueError("%s is on %s, the current device is cuda:%d" % (what, t.device, device))
+    if t.numel() < need:
+        raise ValueError("%s holds %d elements, the call needs %d" % (what, t.numel(), need))
     return ptr
 
 
-def _on_current_device(t, what: str) -> None:
-    """The kernels run on the current device's stream: refuse a tensor of another one."""
-    if t is None or isinstance(t, int):
-        return
-    import torch
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError("%s is on %s, the current device is cuda:%d" % (what, t.device, torch.cuda.current_device()))
+def _pool_elements(desc: "CacheDesc", kv_dtype: int) -> int:
+    n = desc.num_blocks * desc.num_kv_heads * desc.block_size * desc.head_dim
+    return n * 9 // 16 if kv_dtype == PA_KV_E2M1 else n
 
 
-def _rows(t, num_tokens: int, heads: int, desc: "CacheDesc", what: str):
-    """Device pointer of a bf16 tensor of at least num_tokens rows of `heads` heads."""
-    if t is not None and not isinstance(t, int) and t.numel() < num_tokens * heads * desc.head_dim:
-        raise ValueError("%s holds %d elements, %d tokens need %d" % (what, t.numel(), num_tokens,
-                                                                      num_tokens * heads * desc.head_dim))
-    return _dev(t, "bfloat16", what)
+_current_device = None       # index of the current device, once torch is there
+
+
+def _device() -> int:
+    global _current_device
+    if _current_device is None:
+        import torch
+        if not torch.cuda.is_available():
+            return -2                # no tensor's device
+        torch.cuda.init()
+        _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return _current_device()
 
 
 _current_raw_stream = None   # of the current device, once torch is there
@@ -323,9 +338,11 @@ def pa_append_kv_e2m1(k, v, slot_mapping, k_scale: float, v_scale: float, k_cach
                       desc: CacheDesc, stream=None, num_tokens: int | None = None) -> None:
     """Quantizing append into 4-bit pools (uint8, pa_kv_cache_bytes(desc, PA_KV_E2M1) each)."""
     n = int(slot_mapping.shape[0]) if num_tokens is None else int(num_tokens)
-    _check(lib.pa_append_kv_e2m1(_rows(k, n, desc.num_kv_heads, desc, "k"), _rows(v, n, desc.num_kv_heads, desc, "v"),
-                                 _dev(slot_mapping, "int64", "slot_mapping"), n, float(k_scale), float(v_scale),
-                                 _cache(k_cache, desc, "k_cache", _E2M1), _cache(v_cache, desc, "v_cache", _E2M1),
+    at, rows, pool = _device(), n * desc.num_kv_heads * desc.head_dim, _pool_elements(desc, PA_KV_E2M1)
+    _check(lib.pa_append_kv_e2m1(_here(k, "bfloat16", "k", at, rows), _here(v, "bfloat16", "v", at, rows),
+                                 _here(slot_mapping, "int64", "slot_mapping", at, n), n, float(k_scale), float(v_scale),
+                                 _here(k_cache, "uint8", "k_cache", at, pool),
+                                 _here(v_cache, "uint8", "v_cache", at, pool),
                                  ctypes.byref(desc), _stream(stream)), "pa_append_kv_e2m1")
 
 
@@ -334,14 +351,15 @@ def pa_rope_append_kv_e2m1(q, q_out, k, v, positions, slot_mapping, rope_theta: 
                            num_tokens: int | None = None) -> None:
     """RoPE of q (into q_out) and k, and the quantizing append into 4-bit pools, in one pass."""
     n = int(slot_mapping.shape[0]) if num_tokens is None else int(num_tokens)
-    _check(lib.pa_rope_append_kv_e2m1(_rows(q, n, desc.num_q_heads, desc, "q"),
-                                      _rows(q_out, n, desc.num_q_heads, desc, "q_out"),
-                                      _rows(k, n, desc.num_kv_heads, desc, "k"),
-                                      _rows(v, n, desc.num_kv_heads, desc, "v"),
-                                      _dev(positions, "int32", "positions"),
-                                      _dev(slot_mapping, "int64", "slot_mapping"), n, float(rope_theta),
-                                      float(k_scale), float(v_scale), _cache(k_cache, desc, "k_cache", _E2M1),
-                                      _cache(v_cache, desc, "v_cache", _E2M1), ctypes.byref(desc),
+    at, dim, pool = _device(), n * desc.head_dim, _pool_elements(desc, PA_KV_E2M1)
+    rows, q_rows = dim * desc.num_kv_heads, dim * desc.num_q_heads
+    _check(lib.pa_rope_append_kv_e2m1(_here(q, "bfloat16", "q", at, q_rows),
+                                      _here(q_out, "bfloat16", "q_out", at, q_rows),
+                                      _here(k, "bfloat16", "k", at, rows), _here(v, "bfloat16", "v", at, rows),
+                                      _here(positions, "int32", "positions", at, n),
+                                      _here(slot_mapping, "int64", "slot_mapping", at, n), n, float(rope_theta),
+                                      float(k_scale), float(v_scale), _here(k_cache, "uint8", "k_cache", at, pool),
+                                      _here(v_cache, "uint8", "v_cache", at, pool), ctypes.byref(desc),
                                       _stream(stream)), "pa_rope_append_kv_e2m1")
 
 
@@ -349,18 +367,22 @@ def pa_gather_kv_e2m1(k_cache, v_cache, slot_mapping, k_scale: float, v_scale: f
                       stream=None, num_tokens: int | None = None) -> None:
     """The slots' rows of 4-bit pools read back as bf16 into k and v."""
     n = int(slot_mapping.shape[0]) if num_tokens is None else int(num_tokens)
-    _check(lib.pa_gather_kv_e2m1(_cache(k_cache, desc, "k_cache", _E2M1), _cache(v_cache, desc, "v_cache", _E2M1),
-                                 _dev(slot_mapping, "int64", "slot_mapping"), n, float(k_scale), float(v_scale),
-                                 _rows(k, n, desc.num_kv_heads, desc, "k"), _rows(v, n, desc.num_kv_heads, desc, "v"),
+    at, rows, pool = _device(), n * desc.num_kv_heads * desc.head_dim, _pool_elements(desc, PA_KV_E2M1)
+    _check(lib.pa_gather_kv_e2m1(_here(k_cache, "uint8", "k_cache", at, pool),
+                                 _here(v_cache, "uint8", "v_cache", at, pool),
+                                 _here(slot_mapping, "int64", "slot_mapping", at, n), n, float(k_scale), float(v_scale),
+                                 _here(k, "bfloat16", "k", at, rows), _here(v, "bfloat16", "v", at, rows),
                                  ctypes.byref(desc), _stream(stream)), "pa_gather_kv_e2m1")
 
 
 def pa_copy_blocks_e2m1(k_cache, v_cache, copies, desc: CacheDesc, stream=None) -> None:
     """pa_copy_blocks for 4-bit pools."""
     n = int(copies.shape[0])
-    _check(lib.pa_copy_blocks_e2m1(_cache(k_cache, desc, "k_cache", _E2M1), _cache(v_cache, desc, "v_cache", _E2M1),
-                                   _dev(copies, "int32", "copies") if n else None, n, ctypes.byref(desc),
-                                   _stream(stream)), "pa_copy_blocks_e2m1")
+    at, pool = _device(), _pool_elements(desc, PA_KV_E2M1)
+    _check(lib.pa_copy_blocks_e2m1(_here(k_cache, "uint8", "k_cache", at, pool),
+                                   _here(v_cache, "uint8", "v_cache", at, pool),
+                                   _here(copies, "int32", "copies", at, 2 * n) if n else None, n,
+                                   ctypes.byref(desc), _stream(stream)), "pa_copy_blocks_e2m1")
 
 
 def pa_rope_append_kv(q, q_out, k, v, positions, slot_mapping, rope_theta: float, k_cache, v_cache,
@@ -418,11 +440,15 @@ def pa_prefill_ex(q, k_cache, v_cache, block_tables, cu_seqlens_q, context_lens,
                   stream=None) -> None:
     """pa_prefill over a cache of the options' type (bf16, or 4-bit pools with their scales)."""
     n = int(context_lens.shape[0])
-    _check(lib.pa_prefill_ex(_dev(q, "bfloat16", "q"), _cache(k_cache, desc, "k_cache", options),
-                             _cache(v_cache, desc, "v_cache", options), _dev(block_tables, "int32", "block_tables"),
-                             _dev(cu_seqlens_q, "int32", "cu_seqlens_q"), _dev(context_lens, "int32", "context_lens"),
-                             n, int(max_q_len), int(max_context_len), float(scale), _dev(out, "bfloat16", "out"),
-                             _dev(workspace, "uint8", "workspace"), int(workspace.numel()), ctypes.byref(desc),
+    kv_dtype = PA_KV_BF16 if options is None else options.kv_dtype
+    at, pool, cache = _device(), _pool_elements(desc, kv_dtype), "bfloat16" if kv_dtype == PA_KV_BF16 else "uint8"
+    _check(lib.pa_prefill_ex(_here(q, "bfloat16", "q", at), _here(k_cache, cache, "k_cache", at, pool),
+                             _here(v_cache, cache, "v_cache", at, pool),
+                             _here(block_tables, "int32", "block_tables", at, n * desc.max_blocks_per_seq),
+                             _here(cu_seqlens_q, "int32", "cu_seqlens_q", at, n + 1),
+                             _here(context_lens, "int32", "context_lens", at),
+                             n, int(max_q_len), int(max_context_len), float(scale), _here(out, "bfloat16", "out", at),
+                             _here(workspace, "uint8", "workspace", at), workspace.numel(), ctypes.byref(desc),
                              ctypes.byref(options) if options is not None else None, _stream(stream)), "pa_prefill_ex")
 
 
@@ -440,13 +466,15 @@ def pa_cross_attention(q, k_cache, v_cache, block_tables, cu_seqlens_q, encoder_
 
     cu_seqlens_q: int32 [num_seqs + 1] row offsets, or None for one row a sequence (max_q_len 1)."""
     n = int(encoder_lens.shape[0])
-    _on_current_device(k_cache, "k_cache")
-    _check(lib.pa_cross_attention(_dev(q, "bfloat16", "q"), _cache(k_cache, desc, "k_cache"),
-                                  _cache(v_cache, desc, "v_cache"), _dev(block_tables, "int32", "block_tables"),
-                                  _dev(cu_seqlens_q, "int32", "cu_seqlens_q"),
-                                  _dev(encoder_lens, "int32", "encoder_lens"), n, int(max_q_len),
-                                  int(max_encoder_len), float(scale), _dev(out, "bfloat16", "out"),
-                                  _dev(workspace, "uint8", "workspace"), int(workspace.numel()),
+    at, pool = _device(), _pool_elements(desc, PA_KV_BF16)
+    rows = n * desc.num_q_heads * desc.head_dim if cu_seqlens_q is None else 0
+    _check(lib.pa_cross_attention(_here(q, "bfloat16", "q", at, rows), _here(k_cache, "bfloat16", "k_cache", at, pool),
+                                  _here(v_cache, "bfloat16", "v_cache", at, pool),
+                                  _here(block_tables, "int32", "block_tables", at, n * desc.max_blocks_per_seq),
+                                  _here(cu_seqlens_q, "int32", "cu_seqlens_q", at, n + 1),
+                                  _here(encoder_lens, "int32", "encoder_lens", at), n, int(max_q_len),
+                                  int(max_encoder_len), float(scale), _here(out, "bfloat16", "out", at, rows),
+                                  _here(workspace, "uint8", "workspace", at), workspace.numel(),
                                   ctypes.byref(desc), _stream(stream)), "pa_cross_attention")
 
 
