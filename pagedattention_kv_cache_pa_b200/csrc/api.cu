@@ -618,7 +618,7 @@ struct RowsPlan {
 
 static bool rows_plan(int32_t num_seqs, int32_t max_q_len, const pa_cache_desc& d, RowsPlan* r) {
     const int32_t G = d.num_q_heads / d.num_kv_heads;
-    if (G > 16 || max_q_len < 1) return false;
+    if (G > 16 || max_q_len < 1 || (int64_t)num_seqs * ceil_div(max_q_len, 16 / G) > INT32_MAX / 2) return false;
     r->tokens = 16 / G < max_q_len ? 16 / G : max_q_len;
     r->chunks = (max_q_len + r->tokens - 1) / r->tokens;
     r->cols = r->tokens * G;
@@ -709,7 +709,8 @@ extern "C" int pa_prefill_ex(const void* q, const void* k_cache, const void* v_c
         return PA_ERR_WORKSPACE;
     if (options->kernel == PA_PREFILL_ROWS || (options->kernel == PA_PREFILL_AUTO && rows_pay(num_seqs, max_q_len, *desc))) {
         RowsPlan r;
-        if (desc->num_q_heads / desc->num_kv_heads > 16) return PA_ERR_UNSUPPORTED;
+        const int32_t G = desc->num_q_heads / desc->num_kv_heads;
+        if (G > 16 || (int64_t)num_seqs * ceil_div(max_q_len, 16 / G) > INT32_MAX / 2) return PA_ERR_UNSUPPORTED;
         if (!rows_plan(num_seqs, max_q_len, *desc, &r)) return PA_ERR_CUDA;
         if ((int64_t)num_seqs * r.chunks * (desc->num_kv_heads / r.desc_heads) * (max_context_len / 16 + 1) / r.slices >=
             (int64_t)INT32_MAX)

@@ -34,7 +34,8 @@ def test_refusals():
         assert call(**bad) == -1, bad
     for bad in (dict(kv_dtype=pa.PA_KV_E4M3), dict(kernel=pa.PA_PREFILL_MMA), dict(kernel=pa.PA_PREFILL_TCGEN05),
                 dict(d=_desc(head_dim=96)), dict(d=_desc(block_size=24)), dict(d=_desc(block_size=192)),
-                dict(rows=64 * 65535)):
+                dict(rows=64 * 65535), dict(kernel=pa.PA_PREFILL_ROWS, n=65535, rows=2000000),
+                dict(kernel=pa.PA_PREFILL_ROWS, d=_desc(num_q_heads=34))):
         assert call(**bad) == -2, bad
     assert call(ws=None) == -4 and call(size=0) == -4 and call(ws=mis) == -4
     assert call(n=0) == 0 and call(rows=0) == 0
@@ -53,7 +54,7 @@ def h():
 def _case(seed, lens, rows, hq, hkv, d, bs, **kw):
     from tests.test_gpu_e2m1 import Case, normal
     c = Case(seed, lens, hq, hkv, d, bs, **kw)
-    c.rows = list(rows)
+    c.rows, c.kernel = list(rows), pa.PA_PREFILL_AUTO
     c.cu = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
     c.q = normal(np.random.default_rng(seed + 1), int(c.cu[-1]), hq, d, scale=kw.get("q_scale", 1.0))
     return c
@@ -72,7 +73,7 @@ def _device(c, h):
 
 
 def _options(c):
-    return pa.PrefillOptions(kv_dtype=pa.PA_KV_E2M1, k_scale=c.gs[0], v_scale=c.gs[1])
+    return pa.PrefillOptions(kernel=c.kernel, kv_dtype=pa.PA_KV_E2M1, k_scale=c.gs[0], v_scale=c.gs[1])
 
 
 def _workspace(c, most, h):
@@ -120,6 +121,16 @@ def test_few_rows(h, hq, hkv, d, bs, most):
     rows = [most, 1, max(1, most - 1), 0, most, 1, most]
     lens = [most, 1, 40 + most, 9, 517, 1000, 64]
     _check(_case(most + hq, lens, rows, hq, hkv, d, bs), h)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kernel", [pa.PA_PREFILL_ROWS, pa.PA_PREFILL_TCGEN05_WS])
+@pytest.mark.parametrize("hq,hkv,d,bs", [(32, 8, 64, 16), (16, 1, 128, 8), (7, 1, 64, 64), (3, 3, 128, 256)])
+def test_either_kernel(h, kernel, hq, hkv, d, bs):
+    # whatever an automatic call would take: one row up to several chunks of rows, and several tiles of them
+    c = _case(kernel + hq, [1, 18, 40, 300, 700, 64, 129], [1, 18, 3, 0, 130, 64, 1], hq, hkv, d, bs, gs=(1.3, 0.21))
+    c.kernel = kernel
+    _check(c, h)
 
 
 @pytest.mark.gpu
