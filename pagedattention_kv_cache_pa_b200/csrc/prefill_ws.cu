@@ -74,10 +74,11 @@ struct WsCfg {
     static constexpr int kOffK = kOffQ + 2 * kQBytes;      // Q: two buffers (this item's, the next's)
     static constexpr int kOffV = kOffK + kStages * kKVBytes;
     static constexpr int kOffBar = kOffV + kStages * kKVBytes;
-    // barriers (8 bytes each): s_full[2], p_full, o_done[2], drain, q_full[2], o_free,
+    // barriers (8 bytes each): s_full[2], p_full[2], o_done[2], drain, q_full[2], o_free,
     // k_full[S], v_full[S], kv_empty[S]; then the tensor-memory address and the last tile the
-    // TMA warp requested
-    static constexpr int kBars = 9 + 3 * kStages;
+    // TMA warp requested.  P has two, as S has: the scores of tile t + 1 are there before the MMA
+    // thread looks for P_t, and one barrier could pass P_t's phase and P_{t+1}'s before it looked
+    static constexpr int kBars = 10 + 3 * kStages;
     static constexpr int kSmem = kOffBar + kBars * 8 + 16;
     static constexpr int kColS = 0;                         // S: two buffers of 64 fp32 columns
     static constexpr int kColO = 128;                       // O: D fp32 columns
@@ -199,10 +200,10 @@ __global__ void __launch_bounds__(kWsThreads, WsCfg<D>::kMinBlocks)
     const uint32_t s_base = smem_u32(smem);
     const uint32_t s_q = s_base + C::kOffQ, s_k = s_base + C::kOffK, s_v = s_base + C::kOffV;
     constexpr int ST = C::kStages;
-    // barriers: s_full[2], p_full, o_done[2], drain, q_full[2], o_free, then per stage k_full,
+    // barriers: s_full[2], p_full[2], o_done[2], drain, q_full[2], o_free, then per stage k_full,
     // v_full, kv_empty
-    const uint32_t bar_s = s_base + C::kOffBar, bar_p = bar_s + 16, bar_o = bar_s + 24, bar_drain = bar_s + 40,
-                   bar_qf = bar_s + 48, bar_of = bar_s + 64, bar_k = bar_s + 72,
+    const uint32_t bar_s = s_base + C::kOffBar, bar_p = bar_s + 16, bar_o = bar_s + 32, bar_drain = bar_s + 48,
+                   bar_qf = bar_s + 56, bar_of = bar_s + 72, bar_k = bar_s + 80,
                    bar_v = bar_k + 8 * ST, bar_e = bar_v + 8 * ST;
     const uint32_t s_tmem = bar_s + C::kBars * 8;
     volatile int* s_kreq = reinterpret_cast<volatile int*>(smem + C::kOffBar + C::kBars * 8 + 4);
@@ -223,6 +224,7 @@ __global__ void __launch_bounds__(kWsThreads, WsCfg<D>::kMinBlocks)
         mbar_init(bar_s, 1);
         mbar_init(bar_s + 8, 1);
         mbar_init(bar_p, 4);                                 // one arrival per softmax warp
+        mbar_init(bar_p + 8, 4);
         mbar_init(bar_o, 1);
         mbar_init(bar_o + 8, 1);
         mbar_init(bar_drain, 1);
@@ -348,7 +350,7 @@ __global__ void __launch_bounds__(kWsThreads, WsCfg<D>::kMinBlocks)
                 }
                 for (int t = 0; t < nt && ok; ++t) {
                     const int gg = g + t;
-                    ok = mbar_wait(bar_p, (uint32_t)(gg & 1), p.status) && wait_v(gg) &&
+                    ok = mbar_wait(bar_p + 8 * (gg & 1), (uint32_t)((gg >> 1) & 1), p.status) && wait_v(gg) &&
                          (t > 0 || k == 0 || mbar_wait(bar_of, (uint32_t)((k - 1) & 1), p.status));
                     if (!ok) break;
                     tc_fence_after_sync();
@@ -518,7 +520,7 @@ __global__ void __launch_bounds__(kWsThreads, WsCfg<D>::kMinBlocks)
                 }
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar_p);
+                if (lane == 0) mbar_arrive(bar_p + 8 * (gg & 1));
             }
             if (failed || !wait_o(g + it.ntiles - 1)) {
                 failed = true;
