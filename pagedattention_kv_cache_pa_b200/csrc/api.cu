@@ -6,6 +6,7 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "pa.h"
@@ -266,7 +267,7 @@ static PrefillParams prefill_params(const void* q, const void* k_cache, const vo
                                     const int32_t* block_tables, const int32_t* cu_seqlens_q,
                                     const int32_t* lens, int32_t num_seqs, int32_t max_q_len, float scale,
                                     pa_bf16* out, void* workspace, const pa_cache_desc& d) {
-    PrefillParams p;
+    PrefillParams p{};
     p.q = static_cast<const uint16_t*>(q);
     p.k_cache = static_cast<const uint16_t*>(k_cache);
     p.v_cache = static_cast<const uint16_t*>(v_cache);
@@ -758,11 +759,31 @@ extern "C" int pa_prefill_ex(const void* q, const void* k_cache, const void* v_c
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
+// Whether a cross attention call takes the stream of key tiles (few items, 64-dim heads), and its workspace:
+// behind the status word the slices' cuts, and two partial states of 128 rows a slice.
+struct CrossPlan {
+    size_t off_cuts, off_lse, off_o, bytes;
+};
+static bool cross_plan(int32_t num_seqs, int32_t max_q_len, int32_t max_len, const pa_cache_desc& d, CrossPlan* c) {
+    if (d.head_dim != 64 || num_seqs < 1 || max_q_len < 1) return false;
+    const int64_t held = std::min<int64_t>(max_len, (int64_t)d.max_blocks_per_seq * d.block_size);
+    const size_t slices = cross_ws_slices(num_seqs, d.num_kv_heads, d.num_q_heads / d.num_kv_heads, max_q_len, held);
+    const size_t rows = slices * 2 * 128;
+    auto up = [](size_t x) { return (x + kWorkspaceAlign - 1) / kWorkspaceAlign * kWorkspaceAlign; };
+    c->off_cuts = kWorkspaceAlign;
+    c->off_lse = c->off_cuts + up(slices * sizeof(int4));
+    c->off_o = c->off_lse + up(rows * sizeof(float));
+    c->bytes = c->off_o + rows * d.head_dim * sizeof(float);
+    return slices > 0;
+}
+
 extern "C" size_t pa_cross_attention_workspace_size(int32_t num_seqs, int32_t max_q_len, int32_t max_encoder_len,
                                                     const pa_cache_desc* desc) {
     if (check_desc(desc) != PA_OK || num_seqs < 0 || max_q_len < 0 || max_encoder_len < 0) return 0;
     const size_t step = max_q_len == 1 ? pa_decode_workspace_size(num_seqs, max_encoder_len, desc) : 0;
-    return step > kWorkspaceAlign ? step : kWorkspaceAlign;
+    CrossPlan c;
+    return std::max(std::max(kWorkspaceAlign, step),
+                    cross_plan(num_seqs, max_q_len, max_encoder_len, *desc, &c) ? c.bytes : 0);
 }
 
 extern "C" int pa_cross_attention(const pa_bf16* q, const pa_bf16* k_cache, const pa_bf16* v_cache,
@@ -791,8 +812,16 @@ extern "C" int pa_cross_attention(const pa_bf16* q, const pa_bf16* k_cache, cons
         return PA_ERR_INVALID;
     if (!workspace || !aligned(workspace, kWorkspaceAlign) || workspace_bytes < kWorkspaceAlign)
         return PA_ERR_WORKSPACE;
-    const PrefillParams p = prefill_params(q, k_cache, v_cache, block_tables, cu_seqlens_q, encoder_lens, num_seqs,
-                                           max_q_len, scale, out, workspace, *desc);
+    PrefillParams p = prefill_params(q, k_cache, v_cache, block_tables, cu_seqlens_q, encoder_lens, num_seqs,
+                                     max_q_len, scale, out, workspace, *desc);
+    CrossPlan c;
+    if (cross_plan(num_seqs, max_q_len, max_encoder_len, *desc, &c)) {
+        if (workspace_bytes < c.bytes) return PA_ERR_WORKSPACE;
+        char* ws = static_cast<char*>(workspace);
+        p.cuts = reinterpret_cast<int4*>(ws + c.off_cuts);
+        p.part_lse = reinterpret_cast<float*>(ws + c.off_lse);
+        p.part_o = reinterpret_cast<float*>(ws + c.off_o);
+    }
     const cudaError_t e = launch_cross(p, max_q_len, (cudaStream_t)stream);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

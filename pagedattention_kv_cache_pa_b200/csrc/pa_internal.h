@@ -96,6 +96,9 @@ struct PrefillParams {
     int32_t max_q_len;             // the caller's bound on every sequence's query count
     float scale_log2;
     float out_scale;               // multiplies the normalised output (4-bit pools: the V scale)
+    int4* cuts;                    // cross attention over the stream of key tiles (else null): the items cut
+    float* part_lse;               // between slices, and their pieces' states
+    float* part_o;
 };
 cudaError_t launch_prefill(const PrefillParams& p, int max_q_len, cudaStream_t stream);
 cudaError_t launch_prefill_tc(const PrefillParams& p, int max_q_len, cudaStream_t stream);
@@ -103,6 +106,7 @@ cudaError_t launch_prefill_tc(const PrefillParams& p, int max_q_len, cudaStream_
 cudaError_t launch_prefill_ws(const PrefillParams& p, int max_q_len, cudaStream_t stream);
 // cross attention: either kernel's tiles without the causal mask
 cudaError_t launch_cross_ws(const PrefillParams& p, int max_q_len, cudaStream_t stream);
+int cross_ws_slices(int32_t num_seqs, int32_t num_kv_heads, int32_t group, int32_t max_q_len, int64_t max_len);
 cudaError_t launch_cross(const PrefillParams& p, int max_q_len, cudaStream_t stream);
 bool prefill_ws_supports(int block_size);
 

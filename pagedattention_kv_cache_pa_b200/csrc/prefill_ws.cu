@@ -48,6 +48,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstring>
+#include <type_traits>
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
@@ -147,6 +148,7 @@ __device__ __forceinline__ long long ws_index(long long r) {
 // One work item: 128 query rows (a row tile) of one kv head of one sequence.
 struct WsItem {
     int b, kvh, q0, Tq, L, rows, r0, ntiles, pos_first;
+    int t0;                          // stream: its first key tile (not 0: a piece of an item)
 };
 
 // Item i: the t-th row tile from the end of every chunk for t = i / (B Hkv) (the last row
@@ -190,7 +192,135 @@ __device__ __forceinline__ int ws_item(const PrefillParams& p, long long i, WsIt
     return 1;
 }
 
-template <int D, bool kCausal>
+// ---- cross attention of few items: the stream of key tiles ----
+// The items' tiles stand in one row, by sequence, kv head and row tile (a sequence without tokens
+// counts one a row tile), and CTA i of Gc takes tiles [i S / Gc, (i + 1) S / Gc).  An item that lies
+// in one slice is written out; one cut between slices leaves a partial state (normalised fp32 O,
+// log2-domain lse) a piece, joined by cross_merge_kernel.
+constexpr int kMinSlice = 4;         // tiles a slice, below which a cut costs more than it shares out
+
+struct CrossSeq {
+    int q0, Tq, L, row_tiles, nt;    // nt: key tiles, 1 of an empty sequence
+    long long tiles;                 // its share of the stream, 0 for one without queries or with bad lengths
+    bool bad;
+};
+
+__device__ __forceinline__ CrossSeq cross_seq(const PrefillParams& p, int b) {
+    CrossSeq c;
+    c.q0 = p.cu_q[b];
+    c.Tq = p.cu_q[b + 1] - c.q0;
+    c.L = p.context_lens[b];
+    c.bad = c.Tq > 0 && (c.L < 0 || c.L > p.max_blocks_per_seq * p.block_size || c.Tq > p.max_q_len);
+    c.row_tiles = c.Tq <= 0 || c.bad ? 0 : (c.Tq * p.group + kWsRows - 1) / kWsRows;
+    c.nt = c.L > 0 ? (c.L - 1) / kWsKeys + 1 : 1;
+    c.tiles = (long long)c.row_tiles * p.num_kv_heads * c.nt;
+    return c;
+}
+
+// Where the stream is cut (by a whole warp): lane i sums sequences [i cs, (i + 1) cs), a scan joins them.
+struct CrossStream {
+    long long S, Gc, excl, incl;
+    int c_lo;
+
+    __device__ __forceinline__ CrossStream(const PrefillParams& p, int slices, bool report) {
+        const int lane = threadIdx.x & 31, cs = (p.num_seqs + 31) / 32;
+        c_lo = min(p.num_seqs, lane * cs);
+        const int c_hi = min(p.num_seqs, c_lo + cs);
+        long long sum = 0;
+        for (int b = c_lo; b < c_hi; ++b) {
+            const CrossSeq c = cross_seq(p, b);
+            if (c.bad && report) raise_status(p.status, kStatusBadLength);
+            sum += c.tiles;
+        }
+        incl = sum;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += v;
+        }
+        excl = incl - sum;
+        S = __shfl_sync(0xffffffffu, incl, 31);
+        Gc = min((long long)slices, max(1LL, S / kMinSlice));
+    }
+    __device__ __forceinline__ long long lo(long long i) const { return i * S / Gc; }
+    __device__ __forceinline__ long long slice_of(long long u) const { return ((u + 1) * Gc - 1) / S; }
+    // the sequence of tile u < S, and u's distance from its first
+    __device__ __forceinline__ int seq_of(const PrefillParams& p, long long u, long long& rem) const {
+        const int lane = threadIdx.x & 31;
+        const int k = __ffs(__ballot_sync(0xffffffffu, u >= excl && u < incl)) - 1;
+        int b = c_lo;
+        rem = u - excl;
+        if (lane == k)
+            for (long long n; rem >= (n = cross_seq(p, b).tiles); ++b) rem -= n;
+        rem = __shfl_sync(0xffffffffu, rem, k);
+        return __shfl_sync(0xffffffffu, b, k);
+    }
+};
+
+// The walk of one role's warps over its CTA's items.  next() returns 1 for an item to run, 2 (cross
+// attention only) for rows with no token to attend to, 3 for nothing here, 0 at the end.
+template <bool kCausal>
+struct WsWalk {
+    long long r = -1;
+    __device__ __forceinline__ WsWalk(const PrefillParams&, bool) {}
+    __device__ __forceinline__ int next(const PrefillParams& p, long long n_items, WsItem& it, bool report) {
+        const long long i = ws_index(++r);
+        if (i >= n_items) return 0;
+        bool tile0;
+        const int st = ws_item<kCausal>(p, i, it, tile0);
+        if (st < 0 && tile0 && report) raise_status(p.status, kStatusBadLength);
+        return st > 0 ? st : 3;
+    }
+};
+struct WsStream {
+    int left = 0;                    // tiles of the slice to come (fits: few items)
+    int b = 0, m = 0, t = 0;         // sequence, item of it (kv head by kv head), tile of that
+    CrossSeq c;
+    __device__ __forceinline__ WsStream(const PrefillParams& p, bool report) {
+        const CrossStream s(p, gridDim.x, report && blockIdx.x == 0);
+        const bool told = report && (threadIdx.x & 31) == 0;
+        if (told) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
+        if (blockIdx.x >= s.Gc || s.S == 0) return;
+        const long long lo = s.lo(blockIdx.x);
+        left = (int)(s.lo(blockIdx.x + 1) - lo);
+        long long rem;
+        b = s.seq_of(p, lo, rem);
+        c = cross_seq(p, b);
+        m = (int)(rem / c.nt);
+        t = (int)(rem - (long long)m * c.nt);
+        // this slice begins inside an item, and is the second to hold some of it: what there is to join
+        if (told && t > 0 && lo - t >= s.lo(blockIdx.x - 1)) {
+            const int kvh = m / c.row_tiles;
+            p.cuts[blockIdx.x] = make_int4((int)(s.slice_of(lo - t + c.nt - 1) - blockIdx.x) + 2, b, kvh,
+                                           (m - kvh * c.row_tiles) * kWsRows);
+        }
+    }
+    __device__ __forceinline__ int next(const PrefillParams& p, long long, WsItem& it, bool) {
+        if (left <= 0) return 0;
+        it.b = b;
+        it.kvh = m / c.row_tiles;
+        it.r0 = (m - it.kvh * c.row_tiles) * kWsRows;
+        it.q0 = c.q0;
+        it.Tq = c.Tq;
+        it.L = c.L;
+        it.rows = c.Tq * p.group;
+        it.pos_first = c.L - 1;
+        it.t0 = t;
+        it.ntiles = min(left, c.nt - t);
+        left -= it.ntiles;
+        t += it.ntiles;
+        if (t == c.nt) {
+            t = 0;
+            if (++m == c.row_tiles * p.num_kv_heads) {
+                m = 0;
+                if (left > 0) do c = cross_seq(p, ++b); while (c.tiles == 0);
+            }
+        }
+        return it.L > 0 ? 1 : 2;
+    }
+};
+
+template <int D, bool kCausal, bool kStream>
 __global__ void __launch_bounds__(kWsThreads, WsCfg<D>::kMinBlocks)
     prefill_ws_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap) {
@@ -211,6 +341,8 @@ __global__ void __launch_bounds__(kWsThreads, WsCfg<D>::kMinBlocks)
     const int G = p.group, Hq = p.num_q_heads, Hkv = p.num_kv_heads, Bs = p.block_size;
     const long long n_items =
         (long long)p.num_seqs * Hkv * ((p.max_q_len * (long long)G + kWsRows - 1) / kWsRows);
+    using Walk = std::conditional_t<kStream, WsStream, WsWalk<kCausal>>;
+    if (kStream) allow_dependents();                         // the merge kernel waits for this grid's end
 
     if (s_base & 1023u) {                                    // the swizzle needs 1024-byte-aligned tiles
         if (tid == 0) raise_status(p.status, kStatusSmemAlign);
@@ -247,17 +379,15 @@ __global__ void __launch_bounds__(kWsThreads, WsCfg<D>::kMinBlocks)
     bool failed = false;
     int k_seen = -1, v_seen = -1;                            // MMA thread: last K / V tile seen landed
     WsItem it;
-    bool tile0;
 
     if (warp == 5) {
         // ================================ TMA ================================
         // Per item its K and V tiles into the ring; tile counter g runs over items.
         const int rb = Bs < kWsKeys ? Bs : kWsKeys, nslot = kWsKeys / rb;
         int g = 0;
-        for (long long r = 0, i = ws_index(0); i < n_items && !failed; i = ws_index(++r)) {
-            const int st_item = ws_item<kCausal>(p, i, it, tile0);
-            if (st_item < 0 && tile0 && lane == 0) raise_status(p.status, kStatusBadLength);
-            if (st_item != 1) continue;
+        Walk walk(p, true);                                  // (this warp reports, and leaves word of the cuts)
+        for (int kind; !failed && (kind = walk.next(p, n_items, it, lane == 0));) {
+            if (kind != 1) continue;
             const int* table = p.block_tables + (size_t)it.b * p.max_blocks_per_seq;
             for (int t = 0; t < it.ntiles; ++t, ++g) {
                 const int st = g % ST;
@@ -269,7 +399,7 @@ __global__ void __launch_bounds__(kWsThreads, WsCfg<D>::kMinBlocks)
                         break;
                     }
                 }
-                const int kp = t * kWsKeys + lane * rb;
+                const int kp = ((kStream ? it.t0 : 0) + t) * kWsKeys + lane * rb;
                 bool valid = lane < nslot && kp < it.L;
                 int id = valid ? __ldg(table + kp / Bs) : 0;
                 if (valid && (id < 0 || id >= p.num_blocks)) {
@@ -297,6 +427,7 @@ __global__ void __launch_bounds__(kWsThreads, WsCfg<D>::kMinBlocks)
         }
     } else if (warp == 4) {
         // ================================ MMA ================================
+        Walk walk(p, false);
         if (lane == 0) {
             constexpr uint32_t kIdescS = umma_idesc_bf16(kWsRows, kWsKeys, false);
             constexpr uint32_t kIdescO = umma_idesc_bf16(kWsRows, D, true);
@@ -336,8 +467,8 @@ __global__ void __launch_bounds__(kWsThreads, WsCfg<D>::kMinBlocks)
             // previous item's O out of tensor memory
             int g = 0, k = 0;
             bool ok = true;
-            for (long long r = 0, i = ws_index(0); i < n_items && ok; i = ws_index(++r)) {
-                if (ws_item<kCausal>(p, i, it, tile0) != 1) continue;
+            for (int kind; ok && (kind = walk.next(p, n_items, it, false));) {
+                if (kind != 1) continue;
                 const int qb = k & 1, nt = it.ntiles;
                 const uint32_t qbuf = s_q + qb * C::kQBytes;
                 ok = mbar_wait(bar_qf + 8 * qb, (uint32_t)((k >> 1) & 1), p.status) && wait_k(g);
@@ -407,30 +538,41 @@ __global__ void __launch_bounds__(kWsThreads, WsCfg<D>::kMinBlocks)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_qf + 8 * qb);
         };
-        auto next_item = [&](long long& r, WsItem& w) {      // the CTA's next item with work
-            for (long long i = ws_index(++r); i < n_items; i = ws_index(++r)) {
-                const int st_item = ws_item<kCausal>(p, i, w, tile0);
-                if (st_item == 1) return true;
-                if (!kCausal && st_item == 2 && w.r0 + tid < w.rows) {   // nothing to attend to: a zero row
-                    const int R = w.r0 + tid, tok = R / G;
-                    uint4* o = reinterpret_cast<uint4*>(
-                        p.out + ((size_t)(w.q0 + tok) * Hq + (size_t)w.kvh * G + (R - tok * G)) * D);
+        auto zero_rows = [&](const WsItem& w) {              // nothing to attend to
+            const int R = w.r0 + tid, tok = R / G;
+            if (R >= w.rows) return;
+            uint4* o = reinterpret_cast<uint4*>(
+                p.out + ((size_t)(w.q0 + tok) * Hq + (size_t)w.kvh * G + (R - tok * G)) * D);
 #pragma unroll
-                    for (int c = 0; c < kCh; ++c) o[c] = make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < kCh; ++c) o[c] = make_uint4(0, 0, 0, 0);
+        };
+        Walk walk(p, false);
+        long long r = -1;
+        auto next_item = [&](WsItem& w) {                    // the CTA's next item with work
+            if constexpr (kStream) {
+                for (int kind; (kind = walk.next(p, n_items, w, false));) {
+                    if (kind == 1) return true;
+                    zero_rows(w);
+                }
+            } else {                                         // (WsWalk::next in place: it costs no registers here)
+                bool tile0;
+                for (long long i = ws_index(++r); i < n_items; i = ws_index(++r)) {
+                    const int st_item = ws_item<kCausal>(p, i, w, tile0);
+                    if (st_item == 1) return true;
+                    if (!kCausal && st_item == 2) zero_rows(w);
                 }
             }
             return false;
         };
-        long long r = -1;
         WsItem nx;
-        bool has = next_item(r, it);
+        bool has = next_item(it);
         if (has) {
             load_q(it, 0);
             publish_q(0);
         }
         int g = 0, k = 0;
         while (has && !failed) {
-            const bool has_nx = next_item(r, nx);
+            const bool has_nx = next_item(nx);
             if (has_nx) load_q(nx, (k + 1) & 1);
             const int R = it.r0 + tid, L = it.L;
             const int pos = kCausal && R < it.rows ? L - it.Tq + R / G : L - 1;   // padded rows: computed, not written
@@ -444,7 +586,7 @@ __global__ void __launch_bounds__(kWsThreads, WsCfg<D>::kMinBlocks)
                 tc_fence_after_sync();
                 uint32_t sr[64];
                 tmem_ld64(t_lane + C::kColS + (gg & 1) * 64, sr);
-                const int k0 = t * kWsKeys;
+                const int k0 = ((kStream ? it.t0 : 0) + t) * kWsKeys;
                 if (k0 + kWsKeys - 1 > it.pos_first) {       // a tile on the diagonal: mask
 #pragma unroll
                     for (int j = 0; j < 64; ++j)
@@ -531,11 +673,21 @@ __global__ void __launch_bounds__(kWsThreads, WsCfg<D>::kMinBlocks)
             const int tok = R / G, gq = R - tok * G;
             const float inv = 1.f / l_run;
             uint16_t* out = p.out + ((size_t)(it.q0 + tok) * Hq + (size_t)it.kvh * G + gq) * D;
+            // a piece: its state, in the slice's first place if it continues an item, in the second if it begins one
+            const size_t part = ((size_t)blockIdx.x * 2 + (it.t0 == 0 ? 1 : 0)) * kWsRows + tid;
+            const bool piece = kStream && it.ntiles < (L + kWsKeys - 1) / kWsKeys;
+            if (piece) p.part_lse[part] = m_run + __log2f(l_run);
 #pragma unroll
             for (int h = 0; h < D / 32; ++h) {
                 uint32_t o[32];
                 tmem_ld32(t_lane + C::kColO + h * 32, o);   // warp-wide: padded rows join the load
-                if (R < it.rows) {
+                if (piece) {
+                    float4* po = reinterpret_cast<float4*>(p.part_o + part * D + h * 32);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        po[c] = make_float4(__uint_as_float(o[4 * c]) * inv, __uint_as_float(o[4 * c + 1]) * inv,
+                                            __uint_as_float(o[4 * c + 2]) * inv, __uint_as_float(o[4 * c + 3]) * inv);
+                } else if (R < it.rows) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint4 w;
@@ -577,6 +729,41 @@ __global__ void __launch_bounds__(kWsThreads, WsCfg<D>::kMinBlocks)
     }
 }
 
+// The pieces of a cut item, joined: M = max lse, w = 2^(lse - M), out = sum w o / sum w.  CTA (x, y): rows
+// 32 y .. 32 y + 31 of the item that slice x + 1 is the second to hold some of, if there is one.  16 lanes a
+// row hold its 64 dims.
+constexpr int kMergeRows = 32;
+template <int D>
+__global__ void __launch_bounds__(kMergeRows * D / 4) cross_merge_kernel(const PrefillParams p) {
+    constexpr int kLanes = D / 4;
+    wait_prerequisite();
+    const int i = blockIdx.x + 1;
+    const int4 cut = p.cuts[i];
+    const int pieces = cut.x, b = cut.y, kvh = cut.z;
+    if (pieces < 2) return;
+    const int row = blockIdx.y * kMergeRows + threadIdx.x / kLanes, d = threadIdx.x % kLanes * 4;
+    const int R = cut.w + row, q0 = p.cu_q[b], Tq = p.cu_q[b + 1] - q0;
+    if (R >= Tq * p.group) return;
+    float M = 0.f, W = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < pieces; ++k) {
+        const size_t part = (size_t)(k == 0 ? 2 * i - 1 : 2 * (i - 1 + k)) * kWsRows + row;
+        const float lse = p.part_lse[part];
+        const float4 o = *reinterpret_cast<const float4*>(p.part_o + part * D + d);
+        const float mn = k == 0 ? lse : fmaxf(M, lse), a = k == 0 ? 0.f : fast_exp2(M - mn), w = fast_exp2(lse - mn);
+        M = mn;
+        W = W * a + w;
+        acc.x = acc.x * a + w * o.x;
+        acc.y = acc.y * a + w * o.y;
+        acc.z = acc.z * a + w * o.z;
+        acc.w = acc.w * a + w * o.w;
+    }
+    const float inv = 1.f / W;
+    const int tok = R / p.group;
+    *reinterpret_cast<uint2*>(p.out + ((size_t)(q0 + tok) * p.num_q_heads + (size_t)kvh * p.group + (R - tok * p.group)) * D + d) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+}
+
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -611,14 +798,14 @@ bool ws_pool_map(CUtensorMap* map, const void* base, const PrefillParams& p) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool kCausal>
+template <int D, bool kCausal, bool kStream>
 cudaError_t launch_ws(const PrefillParams& p, int max_q_len, cudaStream_t stream) {
     constexpr size_t smem = WsCfg<D>::kSmem;
     static std::atomic<uint64_t> attr_set{0};               // one bit per device
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!(attr_set.load(std::memory_order_acquire) & (1ull << dev))) {
-        const cudaError_t e = cudaFuncSetAttribute(prefill_ws_kernel<D, kCausal>,
+        const cudaError_t e = cudaFuncSetAttribute(prefill_ws_kernel<D, kCausal, kStream>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
         attr_set.fetch_or(1ull << dev, std::memory_order_acq_rel);
@@ -633,10 +820,26 @@ cudaError_t launch_ws(const PrefillParams& p, int max_q_len, cudaStream_t stream
     int sms = 0;
     if (num_sms_current_device(&sms) != PA_OK || sms <= 0) return cudaErrorInvalidDevice;
     const long long items = (long long)p.num_seqs * p.num_kv_heads * tiles;
-    const long long ctas = std::min<long long>(items, (long long)sms * WsCfg<D>::kMinBlocks);
+    const long long resident = (long long)sms * WsCfg<D>::kMinBlocks;
+    const long long ctas = kStream ? resident : std::min<long long>(items, resident);
     dim3 grid((unsigned)ctas);
-    prefill_ws_kernel<D, kCausal><<<grid, kWsThreads, smem, stream>>>(p, km, vm);
-    return cudaGetLastError();
+    prefill_ws_kernel<D, kCausal, kStream><<<grid, kWsThreads, smem, stream>>>(p, km, vm);
+    const cudaError_t e = cudaGetLastError();
+    if constexpr (!kStream) {
+        return e;
+    } else {
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)ctas - 1, kWsRows / kMergeRows);
+        cfg.blockDim = dim3(kMergeRows * D / 4);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, cross_merge_kernel<D>, p);
+    }
 }
 
 }  // namespace
@@ -647,14 +850,32 @@ bool prefill_ws_supports(int block_size) {
 }
 
 cudaError_t launch_prefill_ws(const PrefillParams& p, int max_q_len, cudaStream_t stream) {
-    if (p.head_dim == 64) return launch_ws<64, true>(p, max_q_len, stream);
-    if (p.head_dim == 128) return launch_ws<128, true>(p, max_q_len, stream);
+    if (p.head_dim == 64) return launch_ws<64, true, false>(p, max_q_len, stream);
+    if (p.head_dim == 128) return launch_ws<128, true, false>(p, max_q_len, stream);
     return cudaErrorInvalidValue;
+}
+
+// Slices of the stream of a cross attention call (the workspace holds two partial states of 128 rows
+// each), or 0 where whole items to a CTA are the better way.  A stream saves an item's CTA the tiles that
+// idle ones take, and costs the states' way through memory and the merge, about 16 tiles' time.  Measured
+// (us, stream | whole items): 16 heads, 1 x 4 rows over 1500 tokens 15.2 | 25.0, 1 x 448 23.2 | 25.9, 4 x 200
+// 28.7 | 26.5, 8 x 448 61.4 | 55.7; 8 heads, 1 x 64 over 8000 24.7 | 107, 1 x 4 over 300 15.2 | 9.8; 16 and 2
+// heads, 16 x 5 over 3000 22.8 | 44.6.  (With many items the idle CTAs of the last round are no loss: two
+// CTAs an SM slow one another.)
+int cross_ws_slices(int32_t num_seqs, int32_t num_kv_heads, int32_t group, int32_t max_q_len, int64_t max_len) {
+    int sms = 0;
+    if (num_sms_current_device(&sms) != PA_OK) return 0;
+    const int64_t resident = (int64_t)sms * WsCfg<64>::kMinBlocks;
+    const int64_t row_tiles = ((int64_t)max_q_len * group + kWsRows - 1) / kWsRows;
+    if ((int64_t)num_seqs * num_kv_heads >= resident || row_tiles >= resident) return 0;
+    const int64_t items = (int64_t)num_seqs * num_kv_heads * row_tiles;
+    return items < resident && (max_len + kWsKeys - 1) / kWsKeys * (resident - items) >= 16 * resident ? (int)resident : 0;
 }
 
 cudaError_t launch_cross_ws(const PrefillParams& p, int max_q_len, cudaStream_t stream) {
     // 128 dims: prefill_wide.cu
-    return p.head_dim == 64 ? launch_ws<64, false>(p, max_q_len, stream) : cudaErrorInvalidValue;
+    if (p.head_dim != 64) return cudaErrorInvalidValue;
+    return p.cuts ? launch_ws<64, false, true>(p, max_q_len, stream) : launch_ws<64, false, false>(p, max_q_len, stream);
 }
 
 }  // namespace pa

@@ -98,6 +98,30 @@ def test_more_tiles_than_the_grid_and_masks(h):
     Case(5, [1000], [3], 8, 8, 128, 16, q_scale=6.0).check(h)
 
 
+@pytest.mark.parametrize("lens,rows,hq,hkv,bs", [
+    ([9000], [5], 4, 2, 16),                              # one item cut into many slices
+    ([3001, 0, 70, 1500, 5000], [3, 7, 0, 200, 129], 6, 2, 64),   # empty, without rows, ragged, whole ones among them
+    ([1024, 1025, 1], [128, 128, 128], 3, 3, 128),        # slices that end with items
+    ([2000] * 40, [1, 2] * 20, 2, 1, 8),                  # more sequences than a warp's lanes
+])
+def test_few_items_cut_between_slices(h, lens, rows, hq, hkv, bs):
+    c = Case(len(lens) + hq, lens, rows, hq, hkv, 64, bs)
+    size = pa.pa_cross_attention_workspace_size(len(rows), max(rows), c.longest, c.desc)
+    assert size > 256                                     # the call keeps pieces' states there
+    c.check(h)
+
+
+def test_few_items_report_bad_lengths(h):
+    c = Case(5, [2000, 1900, 2500], [4, 5, 6], 4, 4, 64, 16)
+    ref, tol = c.reference()
+    c.lens[1] = c.mb * 16 + 1
+    got, st = c.run(h)
+    live = np.r_[0:4, 9:15]
+    assert st == -8 and (got[4:9] == 9.0).all() and np.all(np.abs(got - ref)[live] <= tol[live])
+    got, st = c.run(h, max_rows=5)
+    assert st == -8 and (got[4:] == 9.0).all() and np.all(np.abs(got - ref)[:4] <= tol[:4])
+
+
 @pytest.mark.parametrize("hq,hkv,d,bs", [(16, 16, 64, 16), (8, 1, 128, 8), (12, 6, 64, 128)])
 def test_single_rows(h, hq, hkv, d, bs):
     c = Case(9, [1, 64, 0, 300, 77], [1] * 5, hq, hkv, d, bs)
@@ -124,7 +148,8 @@ def test_reported_lengths_leave_rows_unwritten(h):
 
 def test_graph_streams_and_repeats(h):
     cs = [Case(21 + i, [300, 0, 77], [40, 3, 129], 16, 8, 64, 16) for i in range(2)]
-    held = [(*c.device(h), torch.zeros(256, dtype=torch.uint8, device=h.DEV)) for c in cs]
+    held = [(*c.device(h), torch.zeros(pa.pa_cross_attention_workspace_size(3, 129, 300, c.desc), dtype=torch.uint8,
+                                       device=h.DEV)) for c in cs]
     outs = [torch.zeros_like(x[0]) for x in held]
     streams = [torch.cuda.Stream() for _ in cs]
     torch.cuda.synchronize()
