@@ -759,15 +759,16 @@ extern "C" int pa_prefill_ex(const void* q, const void* k_cache, const void* v_c
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
-// Whether a cross attention call takes the stream of key tiles (few items, 64-dim heads), and its workspace:
+// Whether a cross attention call takes the stream of key tiles (few items), and its workspace:
 // behind the status word the slices' cuts, and two partial states of 128 rows a slice.
 struct CrossPlan {
     size_t off_cuts, off_lse, off_o, bytes;
 };
 static bool cross_plan(int32_t num_seqs, int32_t max_q_len, int32_t max_len, const pa_cache_desc& d, CrossPlan* c) {
-    if (d.head_dim != 64 || num_seqs < 1 || max_q_len < 1) return false;
+    if ((d.head_dim != 64 && d.head_dim != 128) || num_seqs < 1 || max_q_len < 1) return false;
     const int64_t held = std::min<int64_t>(max_len, (int64_t)d.max_blocks_per_seq * d.block_size);
-    const size_t slices = cross_ws_slices(num_seqs, d.num_kv_heads, d.num_q_heads / d.num_kv_heads, max_q_len, held);
+    const size_t slices = cross_ws_slices(num_seqs, d.num_kv_heads, d.num_q_heads / d.num_kv_heads, d.head_dim,
+                                          max_q_len, held);
     const size_t rows = slices * 2 * 128;
     auto up = [](size_t x) { return (x + kWorkspaceAlign - 1) / kWorkspaceAlign * kWorkspaceAlign; };
     c->off_cuts = kWorkspaceAlign;

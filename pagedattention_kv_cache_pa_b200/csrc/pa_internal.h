@@ -106,7 +106,8 @@ cudaError_t launch_prefill_tc(const PrefillParams& p, int max_q_len, cudaStream_
 cudaError_t launch_prefill_ws(const PrefillParams& p, int max_q_len, cudaStream_t stream);
 // cross attention: either kernel's tiles without the causal mask
 cudaError_t launch_cross_ws(const PrefillParams& p, int max_q_len, cudaStream_t stream);
-int cross_ws_slices(int32_t num_seqs, int32_t num_kv_heads, int32_t group, int32_t max_q_len, int64_t max_len);
+int cross_ws_slices(int32_t num_seqs, int32_t num_kv_heads, int32_t group, int32_t head_dim,
+                    int32_t max_q_len, int64_t max_len);
 cudaError_t launch_cross(const PrefillParams& p, int max_q_len, cudaStream_t stream);
 bool prefill_ws_supports(int block_size);
 

@@ -804,9 +804,10 @@ cudaError_t launch_prefill_e2m1(const PrefillParams& p, int max_q_len, cudaStrea
 // Cross attention.  With 128 dims these tiles; with 64 dims those of prefill_ws.cu, two CTAs an SM of
 // 128 rows each.  Measured (us, these | prefill_ws.cu), 16 heads: 8 x 448 rows over 1500 tokens, 128
 // dims 67 | 122, 64 dims 59 | 55; 32 x 100 over 500, 128 dims 49 | 52, 64 dims 42 | 25; 32 and 8 heads,
-// 4 x 1024 over 4096, 128 dims 284 (967 TFLOP/s) | 505, 64 dims 264 | 241.
+// 4 x 1024 over 4096, 128 dims 284 (967 TFLOP/s) | 505, 64 dims 264 | 241.  A call of few items (p.cuts)
+// goes to the stream of key tiles there.
 cudaError_t launch_cross(const PrefillParams& p, int max_q_len, cudaStream_t stream) {
-    if (p.head_dim == 128) return launch_w<128, false, false>(p, max_q_len, stream);
+    if (p.head_dim == 128 && !p.cuts) return launch_w<128, false, false>(p, max_q_len, stream);
     return launch_cross_ws(p, max_q_len, stream);
 }
 

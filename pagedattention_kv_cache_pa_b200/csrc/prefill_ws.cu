@@ -26,6 +26,7 @@
 //              stage is refilled once the MMAs that read it have completed.
 // kCausal = false is cross attention: every query row attends to all L tokens of its sequence (an
 // encoder's states), whatever its row count; a sequence without tokens writes zero rows.
+// kStream: a cross attention call of few items, whose key tiles are cut evenly over the CTAs instead.
 //   Q: two buffers.  The softmax warps request the next item's Q rows (cp.async, zeros past
 //   the chunk) when an item starts and publish them when it ends.
 //   An item's first P V, which overwrites O, waits until the softmax warps have read the
@@ -730,8 +731,8 @@ __global__ void __launch_bounds__(kWsThreads, WsCfg<D>::kMinBlocks)
 }
 
 // The pieces of a cut item, joined: M = max lse, w = 2^(lse - M), out = sum w o / sum w.  CTA (x, y): rows
-// 32 y .. 32 y + 31 of the item that slice x + 1 is the second to hold some of, if there is one.  16 lanes a
-// row hold its 64 dims.
+// 32 y .. 32 y + 31 of the item that slice x + 1 is the second to hold some of, if there is one.  D / 4
+// lanes hold a row.
 constexpr int kMergeRows = 32;
 template <int D>
 __global__ void __launch_bounds__(kMergeRows * D / 4) cross_merge_kernel(const PrefillParams p) {
@@ -857,24 +858,26 @@ cudaError_t launch_prefill_ws(const PrefillParams& p, int max_q_len, cudaStream_
 
 // Slices of the stream of a cross attention call (the workspace holds two partial states of 128 rows
 // each), or 0 where whole items to a CTA are the better way.  A stream saves an item's CTA the tiles that
-// idle ones take, and costs the states' way through memory and the merge, about 16 tiles' time.  Measured
-// (us, stream | whole items): 16 heads, 1 x 4 rows over 1500 tokens 15.2 | 25.0, 1 x 448 23.2 | 25.9, 4 x 200
-// 28.7 | 26.5, 8 x 448 61.4 | 55.7; 8 heads, 1 x 64 over 8000 24.7 | 107, 1 x 4 over 300 15.2 | 9.8; 16 and 2
-// heads, 16 x 5 over 3000 22.8 | 44.6.  (With many items the idle CTAs of the last round are no loss: two
-// CTAs an SM slow one another.)
-int cross_ws_slices(int32_t num_seqs, int32_t num_kv_heads, int32_t group, int32_t max_q_len, int64_t max_len) {
+// idle ones take, and costs the states' way through memory and the merge: about 16 tiles' time with 64 dims,
+// 12 with 128.  Measured (us, stream | whole items), 16 heads: 64 dims, 1 x 4 rows over 1500 tokens 15.2 | 25.0,
+// 1 x 448 23.2 | 25.9, 4 x 200 28.7 | 26.5, 8 x 448 61.4 | 55.7; 128 dims (whole items: prefill_wide.cu), 1 x 4
+// 17.6 | 28.7, 1 x 448 31.4 | 33.5, 4 x 200 44.2 | 33.9.  8 heads: 1 x 64 over 8000, 64 dims 24.7 | 107, 128 dims
+// 28.2 | 122; 1 x 4 over 300, 64 dims 15.2 | 9.8, 128 dims 19.3 | 12.1.  (With many items of 64 dims the idle
+// CTAs of the last round are no loss: two CTAs an SM slow one another.)
+int cross_ws_slices(int32_t num_seqs, int32_t num_kv_heads, int32_t group, int32_t head_dim, int32_t max_q_len,
+                    int64_t max_len) {
     int sms = 0;
     if (num_sms_current_device(&sms) != PA_OK) return 0;
-    const int64_t resident = (int64_t)sms * WsCfg<64>::kMinBlocks;
+    const int64_t resident = (int64_t)sms * (head_dim == 64 ? WsCfg<64>::kMinBlocks : WsCfg<128>::kMinBlocks);
     const int64_t row_tiles = ((int64_t)max_q_len * group + kWsRows - 1) / kWsRows;
     if ((int64_t)num_seqs * num_kv_heads >= resident || row_tiles >= resident) return 0;
     const int64_t items = (int64_t)num_seqs * num_kv_heads * row_tiles;
-    return items < resident && (max_len + kWsKeys - 1) / kWsKeys * (resident - items) >= 16 * resident ? (int)resident : 0;
+    return items < resident && (max_len + kWsKeys - 1) / kWsKeys * (resident - items) >= (head_dim == 64 ? 16 : 12) * resident
+               ? (int)resident : 0;
 }
 
 cudaError_t launch_cross_ws(const PrefillParams& p, int max_q_len, cudaStream_t stream) {
-    // 128 dims: prefill_wide.cu
-    if (p.head_dim != 64) return cudaErrorInvalidValue;
+    if (p.head_dim == 128) return launch_ws<128, false, true>(p, max_q_len, stream);   // others: prefill_wide.cu
     return p.cuts ? launch_ws<64, false, true>(p, max_q_len, stream) : launch_ws<64, false, false>(p, max_q_len, stream);
 }
 

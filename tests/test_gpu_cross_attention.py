@@ -104,8 +104,9 @@ def test_more_tiles_than_the_grid_and_masks(h):
     ([1024, 1025, 1], [128, 128, 128], 3, 3, 128),        # slices that end with items
     ([2000] * 40, [1, 2] * 20, 2, 1, 8),                  # more sequences than a warp's lanes
 ])
-def test_few_items_cut_between_slices(h, lens, rows, hq, hkv, bs):
-    c = Case(len(lens) + hq, lens, rows, hq, hkv, 64, bs)
+@pytest.mark.parametrize("d", [64, 128])
+def test_few_items_cut_between_slices(h, lens, rows, hq, hkv, bs, d):
+    c = Case(len(lens) + hq, lens, rows, hq, hkv, d, bs)
     size = pa.pa_cross_attention_workspace_size(len(rows), max(rows), c.longest, c.desc)
     assert size > 256                                     # the call keeps pieces' states there
     c.check(h)
