@@ -406,8 +406,8 @@ PA_API int pa_prefill_ex(const void* q, const void* k_cache, const void* v_cache
  * K_j, V_j of kv head h / (Hq/Hkv).  A sequence without encoder tokens outputs zero rows.
  * cu_seqlens_q as for pa_prefill; NULL (with max_q_len == 1): one query row a sequence, the
  * decoding step, which runs the decode kernels (shapes as for pa_decode) and is the form to use
- * there.  max_q_len >= every row count; max_encoder_len >= every encoder length (used by the
- * NULL form only).  workspace: pa_cross_attention_workspace_size bytes, 256-byte aligned,
+ * there.  max_q_len >= every row count; max_encoder_len >= every encoder length (a longer one is
+ * clipped to it by the NULL form; else it only chooses how the work is shared out).  workspace: pa_cross_attention_workspace_size bytes, 256-byte aligned,
  * zero-filled before its first use, one per call in flight; its status word as for pa_decode
  * (more rows than max_q_len, or a length below zero or past the table: that sequence's rows are
  * left unwritten, or for the NULL form the length clipped, and pa_decode_status reports it).
