@@ -651,6 +651,34 @@ static bool rows_pay(int32_t num_seqs, int32_t max_q_len, const pa_cache_desc& d
     return 10 * chunks * pairs <= 22 * sms * waves;
 }
 
+// Workspace of a call whose items are cut between CTAs: behind the status word which items are, and the
+// pieces' partial states, `rows` of them.
+struct CutPlan {
+    size_t off_cuts, off_lse, off_o, bytes;
+    void apply(PrefillParams& p, void* workspace) const {
+        if (bytes == kWorkspaceAlign) return;
+        char* ws = static_cast<char*>(workspace);
+        p.cuts = reinterpret_cast<int4*>(ws + off_cuts);
+        p.part_lse = reinterpret_cast<float*>(ws + off_lse);
+        p.part_o = reinterpret_cast<float*>(ws + off_o);
+    }
+};
+static CutPlan cut_plan(int ctas, size_t rows, int32_t head_dim) {
+    auto up = [](size_t x) { return (x + kWorkspaceAlign - 1) / kWorkspaceAlign * kWorkspaceAlign; };
+    CutPlan c;
+    c.off_cuts = kWorkspaceAlign;
+    c.off_lse = c.off_cuts + up(ctas * sizeof(int4));
+    c.off_o = c.off_lse + up(rows * sizeof(float));
+    c.bytes = c.off_o + rows * head_dim * sizeof(float);
+    return c;
+}
+static CutPlan prefill_plan(int32_t num_seqs, int32_t max_q_len, int32_t max_len, const pa_cache_desc& d) {
+    const int64_t held = std::min<int64_t>(max_len, (int64_t)d.max_blocks_per_seq * d.block_size);
+    const int ctas = wide_split_ctas(num_seqs, d.num_kv_heads, d.num_q_heads / d.num_kv_heads, d.head_dim,
+                                     max_q_len, held);
+    return cut_plan(ctas, wide_split_rows(ctas), d.head_dim);
+}
+
 static int check_prefill_options(const pa_prefill_options* o) {
     if (!o) return PA_OK;
     if (o->kernel < PA_PREFILL_AUTO || o->kernel > PA_PREFILL_ROWS) return PA_ERR_INVALID;
@@ -674,6 +702,8 @@ extern "C" size_t pa_prefill_workspace_size(int32_t num_seqs, int32_t max_q_len,
         RowsPlan r;
         if (check_e2m1_desc(desc) != PA_OK) return 0;
         if (max_q_len > 0 && num_seqs > 0) return rows_plan(num_seqs, max_q_len, *desc, &r) ? r.bytes : 0;
+    } else if (options && options->kv_dtype == PA_KV_E2M1) {
+        return prefill_plan(num_seqs, max_q_len, max_context_len, *desc).bytes;
     }
     return kWorkspaceAlign;
 }
@@ -755,36 +785,28 @@ extern "C" int pa_prefill_ex(const void* q, const void* k_cache, const void* v_c
     PrefillParams p = prefill_params(q, k_cache, v_cache, block_tables, cu_seqlens_q, context_lens, num_seqs,
                                      max_q_len, scale * options->k_scale, out, workspace, *desc);
     p.out_scale = options->v_scale;
+    const CutPlan c = prefill_plan(num_seqs, max_q_len, max_context_len, *desc);
+    if (workspace_bytes < c.bytes) return PA_ERR_WORKSPACE;
+    c.apply(p, workspace);
     const cudaError_t e = launch_prefill_e2m1(p, max_q_len, (cudaStream_t)stream);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
-// Whether a cross attention call takes the stream of key tiles (few items), and its workspace:
-// behind the status word the slices' cuts, and two partial states of 128 rows a slice.
-struct CrossPlan {
-    size_t off_cuts, off_lse, off_o, bytes;
-};
-static bool cross_plan(int32_t num_seqs, int32_t max_q_len, int32_t max_len, const pa_cache_desc& d, CrossPlan* c) {
-    if ((d.head_dim != 64 && d.head_dim != 128) || num_seqs < 1 || max_q_len < 1) return false;
-    const int64_t held = std::min<int64_t>(max_len, (int64_t)d.max_blocks_per_seq * d.block_size);
-    const size_t slices = cross_ws_slices(num_seqs, d.num_kv_heads, d.num_q_heads / d.num_kv_heads, d.head_dim,
-                                          max_q_len, held);
-    const size_t rows = slices * 2 * 128;
-    auto up = [](size_t x) { return (x + kWorkspaceAlign - 1) / kWorkspaceAlign * kWorkspaceAlign; };
-    c->off_cuts = kWorkspaceAlign;
-    c->off_lse = c->off_cuts + up(slices * sizeof(int4));
-    c->off_o = c->off_lse + up(rows * sizeof(float));
-    c->bytes = c->off_o + rows * d.head_dim * sizeof(float);
-    return slices > 0;
+// Workspace of a cross attention call: calls of few items take the stream of key tiles.
+static CutPlan cross_plan(int32_t num_seqs, int32_t max_q_len, int32_t max_len, const pa_cache_desc& d) {
+    int slices = 0;
+    if ((d.head_dim == 64 || d.head_dim == 128) && num_seqs > 0 && max_q_len > 0) {
+        const int64_t held = std::min<int64_t>(max_len, (int64_t)d.max_blocks_per_seq * d.block_size);
+        slices = cross_ws_slices(num_seqs, d.num_kv_heads, d.num_q_heads / d.num_kv_heads, d.head_dim, max_q_len, held);
+    }
+    return cut_plan(slices, (size_t)slices * 2 * 128, d.head_dim);
 }
 
 extern "C" size_t pa_cross_attention_workspace_size(int32_t num_seqs, int32_t max_q_len, int32_t max_encoder_len,
                                                     const pa_cache_desc* desc) {
     if (check_desc(desc) != PA_OK || num_seqs < 0 || max_q_len < 0 || max_encoder_len < 0) return 0;
     const size_t step = max_q_len == 1 ? pa_decode_workspace_size(num_seqs, max_encoder_len, desc) : 0;
-    CrossPlan c;
-    return std::max(std::max(kWorkspaceAlign, step),
-                    cross_plan(num_seqs, max_q_len, max_encoder_len, *desc, &c) ? c.bytes : 0);
+    return std::max(step, cross_plan(num_seqs, max_q_len, max_encoder_len, *desc).bytes);
 }
 
 extern "C" int pa_cross_attention(const pa_bf16* q, const pa_bf16* k_cache, const pa_bf16* v_cache,
@@ -815,14 +837,9 @@ extern "C" int pa_cross_attention(const pa_bf16* q, const pa_bf16* k_cache, cons
         return PA_ERR_WORKSPACE;
     PrefillParams p = prefill_params(q, k_cache, v_cache, block_tables, cu_seqlens_q, encoder_lens, num_seqs,
                                      max_q_len, scale, out, workspace, *desc);
-    CrossPlan c;
-    if (cross_plan(num_seqs, max_q_len, max_encoder_len, *desc, &c)) {
-        if (workspace_bytes < c.bytes) return PA_ERR_WORKSPACE;
-        char* ws = static_cast<char*>(workspace);
-        p.cuts = reinterpret_cast<int4*>(ws + c.off_cuts);
-        p.part_lse = reinterpret_cast<float*>(ws + c.off_lse);
-        p.part_o = reinterpret_cast<float*>(ws + c.off_o);
-    }
+    const CutPlan c = cross_plan(num_seqs, max_q_len, max_encoder_len, *desc);
+    if (workspace_bytes < c.bytes) return PA_ERR_WORKSPACE;
+    c.apply(p, workspace);
     const cudaError_t e = launch_cross(p, max_q_len, (cudaStream_t)stream);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

@@ -96,8 +96,8 @@ struct PrefillParams {
     int32_t max_q_len;             // the caller's bound on every sequence's query count
     float scale_log2;
     float out_scale;               // multiplies the normalised output (4-bit pools: the V scale)
-    int4* cuts;                    // cross attention over the stream of key tiles (else null): the items cut
-    float* part_lse;               // between slices, and their pieces' states
+    int4* cuts;                    // a call whose items are cut between CTAs (else null): which, and their
+    float* part_lse;               // pieces' states
     float* part_o;
 };
 cudaError_t launch_prefill(const PrefillParams& p, int max_q_len, cudaStream_t stream);
@@ -109,6 +109,10 @@ cudaError_t launch_cross_ws(const PrefillParams& p, int max_q_len, cudaStream_t 
 int cross_ws_slices(int32_t num_seqs, int32_t num_kv_heads, int32_t group, int32_t head_dim,
                     int32_t max_q_len, int64_t max_len);
 cudaError_t launch_cross(const PrefillParams& p, int max_q_len, cudaStream_t stream);
+// CTAs that share the last round's items of prefill_wide.cu (0: they are not cut), rows of partial states
+int wide_split_ctas(int32_t num_seqs, int32_t num_kv_heads, int32_t group, int32_t head_dim, int32_t max_q_len,
+                    int64_t max_len);
+size_t wide_split_rows(int ctas);
 bool prefill_ws_supports(int block_size);
 
 constexpr size_t kWorkspaceAlign = 256;

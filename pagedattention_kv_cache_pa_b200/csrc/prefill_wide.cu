@@ -32,15 +32,19 @@
 //                   products run, the other's softmax has the exponential unit to itself.
 // K and V tiles have rings of their own.
 //
+// Long prefills of few items: the items of the last, unfilled round are cut (Walk, wide_split_ctas).
+//
 // Every wait is bounded (2 s, then the timeout status bit); the tensor memory is freed and no
 // asynchronous operation is left when a CTA exits.
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <stdint.h>
 
 #include <algorithm>
 #include <atomic>
 #include <cstring>
+#include <type_traits>
 
 #include "pa_device.cuh"
 #include "pa_e2m1.cuh"
@@ -57,8 +61,8 @@ constexpr int kKeys = 128;
 constexpr int kLoad0 = 8, kMmaWarp = 12;   // first K/V warp, the MMA warp
 constexpr int kThreads = 512;              // four warpgroups: softmax 0, softmax 1, K/V, MMA
 // Registers a thread: 128 at launch, moved from the last two warpgroups to the softmax ones.  The
-// shares add up to the launch's: 2 x 168 + 112 + 64 = 4 x 128.
-constexpr int kLaunchRegs = 128, kSoftmaxRegs = 168, kLoadRegs = 112, kMmaRegs = 64;
+// shares add up to the launch's: 2 x 168 + 120 + 56 = 4 x 128.
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 168, kLoadRegs = 120, kMmaRegs = 56;
 static_assert(2 * kSoftmaxRegs + kLoadRegs + kMmaRegs == 4 * kLaunchRegs, "register shares");
 constexpr float kRescaleLog2 = 8.f;
 
@@ -143,7 +147,9 @@ __device__ __forceinline__ long long item_index(long long r) {
 // One work item: up to 256 query rows of one kv head of one sequence.
 struct Item {
     int b, kvh, q0, Tq, L, rows, r0;
-    int nt[2];                             // key tiles of either row tile (0: no rows)
+    int nt[2];                             // key tiles of either row tile (0: no rows, or none in this piece)
+    int t0;                                // first key tile: not 0 for a piece that continues an item
+    bool piece;                            // not all of the item's tiles
 };
 
 // Item i, as in prefill_ws.cu: the last row tiles of every chunk first.  1: an item to run; 0: none;
@@ -180,10 +186,116 @@ __device__ __forceinline__ int get_item(const PrefillParams& p, long long i, Ite
         const int seen = kCausal ? it.L - it.Tq + last_tok + 1 : it.L;
         it.nt[g] = first < it.rows ? (seen + kKeys - 1) / kKeys : 0;
     }
+    it.t0 = 0;
+    it.piece = false;
     return it.L > 0 ? 1 : 2;
 }
 
-template <int D, bool kE2m1, bool kCausal>
+// Partial states of 128 rows lie four dims of all rows after the next four: dims 4 i .. 4 i + 3 of state row
+// `part` are [i kRows] from here on.
+template <int D>
+__device__ __forceinline__ float4* part_dims(float* part_o, size_t part) {
+    return reinterpret_cast<float4*>(part_o) + part / kRows * kRows * (D / 4) + part % kRows;
+}
+
+// The walk of one role's warps over its CTA's items.  next() returns 1 for an item to run, 2 (cross
+// attention) for rows with no token, 3 for nothing here, 0 at the end.
+//
+// kSplit: whole items only as long as there is one for every CTA.  The items of the last, unfilled round
+// (fewer than CTAs) are cut: their key tiles stand in one row, of which CTA i of Gc takes tiles
+// [i S / Gc, (i + 1) S / Gc).  An item cut between CTAs leaves a partial state (normalised fp32 O, log2-domain
+// lse) a piece, joined by wide_merge_kernel; p.cuts says which.
+constexpr int kMinSlice = 2;               // tiles a CTA at least
+
+template <bool kCausal, bool kSplit>
+struct Walk {
+    std::conditional_t<kSplit, int, long long> r = -1;   // round (32 bits with kSplit: wide_split_ctas)
+    uint32_t left = 0;                     // tiles of the slice to come
+    int idx = 0, t = 0;                    // item of the last round, tile of it
+    __device__ __forceinline__ Walk(const PrefillParams& p, long long n_items, bool report) {
+        if (kSplit) cut(p, n_items, report);
+    }
+    static __device__ __forceinline__ long long base(long long n_items) {   // the first item of the last round
+        return n_items - n_items % gridDim.x;
+    }
+    static __device__ __forceinline__ int get(const PrefillParams& p, long long i, Item& it, bool report) {
+        bool tile0;
+        const int st = get_item<kCausal>(p, i, it, tile0);
+        if (report && st < 0 && tile0) raise_status(p.status, kStatusBadLength);
+        return st > 0 ? st : 3;
+    }
+    static __device__ __forceinline__ int tiles(int st, const Item& it) {
+        return st == 1 ? max(it.nt[0], it.nt[1]) : st == 2 ? 1 : 0;
+    }
+    // by a whole warp, once and before its work (beside it, the registers are not to be had): this CTA's
+    // slice of the last round
+    __device__ __forceinline__ void cut(const PrefillParams& p, long long n_items, bool report) {
+        const long long base = Walk::base(n_items);
+        const int R = (int)(n_items - base), lane = threadIdx.x & 31, per = (R + 31) / 32;
+        const int first = min(R, lane * per), end = min(R, first + per);
+        Item it;
+        uint32_t sum = 0;                  // fewer items than CTAs, each of at most 2^24 tiles: 32 bits hold them
+        for (int j = first; j < end; ++j) sum += tiles(get(p, base + j, it, report), it);
+        uint32_t incl = sum;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += v;
+        }
+        const unsigned long long S = __shfl_sync(0xffffffffu, incl, 31);
+        const unsigned long long Gc = min((unsigned long long)gridDim.x, max(1ull, S / kMinSlice)), me = blockIdx.x;
+        const bool told = report && lane == 0;
+        if (told) p.cuts[me] = make_int4(0, 0, 0, 0);
+        if (me >= Gc || S == 0) return;
+        const uint32_t lo = (uint32_t)(me * S / Gc), lo_before = me ? (uint32_t)((me - 1) * S / Gc) : 0;
+        left = (uint32_t)((me + 1) * S / Gc) - lo;
+        const int k = __ffs(__ballot_sync(0xffffffffu, lo >= incl - sum && lo < incl)) - 1;
+        int nt = 0;
+        idx = first;
+        if (lane == k) {
+            uint32_t rem = lo - (incl - sum);
+            while (rem >= (uint32_t)(nt = tiles(get(p, base + idx, it, false), it))) rem -= nt, ++idx;
+            t = (int)rem;
+        }
+        idx = __shfl_sync(0xffffffffu, idx, k);
+        t = __shfl_sync(0xffffffffu, t, k);
+        nt = __shfl_sync(0xffffffffu, nt, k);
+        // the slice begins inside an item, and is the second to hold some of it: what there is to join
+        if (told && t > 0 && lo - t >= lo_before) {
+            get(p, base + idx, it, false);
+            const unsigned long long last = ((lo - t + (unsigned long long)nt) * Gc - 1) / S;
+            p.cuts[me] = make_int4((int)(last - me) + 2, it.b, it.kvh, it.r0);
+        }
+    }
+    __device__ __forceinline__ int next(const PrefillParams& p, long long n_items, Item& it, bool report) {
+        if (!kSplit) {
+            const long long i = item_index(++r);
+            return i < n_items ? get(p, i, it, report) : 0;
+        }
+        const long long base = Walk::base(n_items);
+        if ((r + 1LL) * gridDim.x < base) return get(p, item_index(++r), it, report);
+        if (left == 0) return 0;
+        const int st = get(p, base + idx, it, false), nt = tiles(st, it);
+        if (nt == 0) {
+            ++idx;
+            return 3;
+        }
+        const int n = (int)min(left, (uint32_t)(nt - t));
+        it.t0 = t;
+        it.piece = n < nt;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) it.nt[g] = max(0, min(it.nt[g] - t, n));
+        left -= n;
+        t += n;
+        if (t == nt) {
+            t = 0;
+            ++idx;
+        }
+        return st;
+    }
+};
+
+template <int D, bool kE2m1, bool kCausal, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_wide_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap) {
@@ -206,6 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const long long n_items =
         (long long)p.num_seqs * Hkv * ((p.max_q_len * (long long)G + kItemRows - 1) / kItemRows);
 
+    if (kSplit) allow_dependents();                          // the merge kernel waits for this grid's end
     if (s_base & 1023u) {                                    // the swizzle needs 1024-byte-aligned tiles
         if (tid == 0) raise_status(p.status, kStatusSmemAlign);
         return;
@@ -239,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t tmem;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(s_tmem) : "memory");
     tmem = __shfl_sync(0xffffffffu, tmem, 0);
-    bool tile0;
+    using W = Walk<kCausal, kSplit>;
 
     if (warp >= kLoad0 && warp < kMmaWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
@@ -251,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int bs_shift = 31 - __clz(Bs);
             const uint8_t* kc = reinterpret_cast<const uint8_t*>(p.k_cache);
             const uint8_t* vc = reinterpret_cast<const uint8_t*>(p.v_cache);
-            struct Cur {                                     // a tile, and the block of this thread's key
+            struct Cur {                                     // a key tile, and the block of this thread's key
                 Item it;
                 int t, id;
                 bool has;
@@ -260,9 +373,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint4 k[kBlk], v[kBlk];
                 uint32_t ks[kBlk], vs[kBlk];                 // two scale bytes a block, one per half word
             };
-            long long r = -1;
+            W walk(p, n_items, warp == kLoad0);
             auto lookup = [&](Cur& c) {
-                const int kp = c.t * kKeys + key;
+                const int kp = (c.it.t0 + c.t) * kKeys + key;
                 c.id = -1;
                 if (c.has && kp < c.it.L)
                     c.id = __ldg(p.block_tables + (size_t)c.it.b * p.max_blocks_per_seq + (kp >> bs_shift));
@@ -274,19 +387,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return;
                 }
                 n.has = false;
-                for (long long i = item_index(++r); i < n_items; i = item_index(++r)) {
-                    const int st = get_item<kCausal>(p, i, n.it, tile0);
-                    if (st < 0 && tile0 && key == 0) raise_status(p.status, kStatusBadLength);
+                n.t = 0;
+                for (int st; (st = walk.next(p, n_items, n.it, warp == kLoad0));)
                     if (st == 1) {
                         n.has = true;
-                        n.t = 0;
                         break;
                     }
-                }
                 lookup(n);
             };
             auto load = [&](const Cur& c, Raw& x) {
-                bool ok = c.has && c.t * kKeys + key < c.it.L;
+                const int kp = (c.it.t0 + c.t) * kKeys + key;
+                bool ok = c.has && kp < c.it.L;
                 if (ok && (c.id < 0 || c.id >= p.num_blocks)) {
                     raise_status(p.status, kStatusBadBlock);
                     ok = false;
@@ -297,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     x.ks[i] = x.vs[i] = 0u;
                 }
                 if (!ok) return;
-                const int off = (c.t * kKeys + key) & (Bs - 1);
+                const int off = kp & (Bs - 1);
                 const size_t page = ((size_t)c.id * Hkv + c.it.kvh) * page_bytes;
                 const size_t row = page + off * (D / 2), sc = page + Bs * (D / 2) + off;
 #pragma unroll
@@ -364,7 +475,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             Cur a, b;
             Raw xa, xb;
             a.has = false;
-            a.t = 0;
             next(a, a);
             load(a, xa);
             next(a, b);
@@ -385,14 +495,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int u = 0; u < ST; ++u) k_last[u] = v_last[u] = -1;
             Item it;
             bool ok = true, tail_out = false;
-            for (long long r = 0, i = item_index(0); i < n_items && ok; i = item_index(++r)) {
-                const int st_item = get_item<kCausal>(p, i, it, tile0);
-                if (st_item < 0 && tile0 && lane == 0) raise_status(p.status, kStatusBadLength);
-                if (st_item != 1) continue;
+            W walk(p, n_items, true);
+            for (int kind; ok && (kind = walk.next(p, n_items, it, true));) {
+                if (kind != 1) continue;
                 const int* table = p.block_tables + (size_t)it.b * p.max_blocks_per_seq;
                 const int nt = max(it.nt[0], it.nt[1]);
                 for (int t = 0; t < nt && ok; ++t, ++g) {
-                    const int st = g % ST, kp = t * kKeys + lane * rb;
+                    const int st = g % ST, kp = (it.t0 + t) * kKeys + lane * rb;
                     bool valid = lane < nslot && kp < it.L;
                     const int id = valid ? __ldg(table + kp / Bs) : 0;
                     if (valid && (id < 0 || id >= p.num_blocks)) {
@@ -414,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         bar_kf + 8 * st);
                     if (g >= ST && !(ok = warp_wait(bar_ve + 8 * st, par, p.status))) break;
                     // rows of V past the sequence are zeroed once the tile has landed, before it is published
-                    const int in = it.L - t * kKeys;
+                    const int in = it.L - (it.t0 + t) * kKeys;
                     const uint32_t vbar = in < kKeys ? bar_tail : bar_vf + 8 * st;
                     if (lane == 0) mbar_arrive_expect_tx(vbar, bytes);
                     __syncwarp();
@@ -485,8 +594,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             };
             Item it;
-            for (long long r = 0, i = item_index(0); i < n_items && ok; i = item_index(++r)) {
-                if (get_item<kCausal>(p, i, it, tile0) != 1) continue;
+            W walk(p, n_items, false);
+            for (int kind; ok && (kind = walk.next(p, n_items, it, false));) {
+                if (__shfl_sync(0xffffffffu, kind, 0) != 1) continue;
                 const int n0 = __shfl_sync(0xffffffffu, it.nt[0], 0), n1 = __shfl_sync(0xffffffffu, it.nt[1], 0);
                 const int nt = max(n0, n1);
                 // the first scores of either row tile
@@ -546,6 +656,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t t_s = t_lane + C::kColS + gr * kKeys, t_p = t_lane + C::kColP + gr * C::kStepP, t_o = t_lane + C::kColO + gr * D;
         const float sl2 = p.scale_log2;
         auto wait_o = [&](int tt) { return warp_wait(bar_o(gr), (uint32_t)(tt & 1), p.status); };
+        // a piece's state: in the CTA's first place if it continues an item, in the second if it begins one
+        auto part_row = [&](const Item& w) {
+            return ((size_t)blockIdx.x * 2 + (w.t0 == 0 ? 1 : 0)) * kItemRows + gr * kRows + tr;
+        };
         constexpr int kRowStep = kRows / kCh;
         auto load_q = [&](const Item& w, int buf) {
             const uint32_t qbuf = s_q + (2 * buf + gr) * C::kQBytes;
@@ -574,11 +688,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_q(buf, gr));
         };
-        auto next_item = [&](long long& r, Item& w) {        // the CTA's next item with rows for this group
-            for (long long i = item_index(++r); i < n_items; i = item_index(++r)) {
-                const int st = get_item<kCausal>(p, i, w, tile0);
-                if (st == 1 && w.nt[gr] > 0) return true;
+        W walk(p, n_items, false);
+        auto next_item = [&](Item& w) {                      // the CTA's next item with rows for this group
+            for (int st; (st = walk.next(p, n_items, w, false));) {
+                if (st == 1 && (gr ? w.nt[1] : w.nt[0]) > 0) return true;
                 const int R = w.r0 + gr * kRows + tr;
+                if (kSplit && st == 1 && w.piece)            // only tiles behind this row tile's last
+                    p.part_lse[part_row(w)] = -FLT_MAX;
                 if (!kCausal && st == 2 && R < w.rows) {     // nothing to attend to: a zero row
                     const int tok = R / G;
                     uint4* o = reinterpret_cast<uint4*>(
@@ -589,21 +705,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             return false;
         };
-        long long r = -1;
         Item it, nx;
-        bool has = next_item(r, it), failed = false;
+        bool has = next_item(it), failed = false;
         if (has) {
             load_q(it, 0);
             publish_q(0);
         }
         int tt = 0, k = 0;                                   // tiles and items so far
         while (has && !failed) {
-            const bool has_nx = next_item(r, nx);
+            const bool has_nx = next_item(nx);
             if (QB == 2 && has_nx) load_q(nx, (k + 1) & 1);
-            const int R = it.r0 + gr * kRows + tr, L = it.L, nt = it.nt[gr];
+            const int R = it.r0 + gr * kRows + tr, L = it.L, nt = gr ? it.nt[1] : it.nt[0];
             const int pos = kCausal && R < it.rows ? L - it.Tq + R / G : L - 1;   // padded rows: computed, not written
             const int pos_first = kCausal ? L - it.Tq + (it.r0 + gr * kRows) / G : L - 1;
-            float m_run = -INFINITY, l_run = 0.f;
+            // finite from the start: a piece may begin behind a row's last key (weights 2^-inf = 0, not NaN)
+            float m_run = kSplit ? -FLT_MAX : -INFINITY, l_run = 0.f;
             for (int t = 0; t < nt; ++t, ++tt) {
                 if (!warp_wait(bar_s(gr), (uint32_t)(tt & 1), p.status)) {
                     failed = true;
@@ -612,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after_sync();
                 // one Q buffer: the item's last scores are there, so the next item's rows may come
                 if (QB == 1 && has_nx && t == nt - 1) load_q(nx, 0);
-                const int k0 = t * kKeys;
+                const int k0 = (it.t0 + t) * kKeys;
                 const bool diag = k0 + kKeys - 1 > pos_first;   // a tile on the diagonal, or the last: mask
                 uint32_t sr[64];
                 auto mask = [&](int from) {
@@ -633,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mq[(j >> 1) & 3] = fmax3(mq[(j >> 1) & 3], __uint_as_float(sr[j]), __uint_as_float(sr[j + 1]));
                 }
                 const float mx = fmax3(mq[0], mq[1], fmaxf(mq[2], mq[3]));
-                const float m_new = fmaxf(m_run, mx * sl2);  // finite: key 0 is in every row's range
+                const float m_new = fmaxf(m_run, mx * sl2);  // finite: key 0 is in every row's range (pieces: above)
                 if (t == 0) {
                     m_run = m_new;
                 } else {
@@ -694,13 +810,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_after_sync();
             const int tok = R / G, gq = R - tok * G;
-            const float inv = p.out_scale / l_run;
+            const float inv = kSplit && l_run == 0.f ? 0.f : p.out_scale / l_run;
+            const size_t part = part_row(it);
+            if (kSplit && it.piece) p.part_lse[part] = l_run == 0.f ? -FLT_MAX : m_run + __log2f(l_run);
             uint16_t* out = p.out + ((size_t)(it.q0 + tok) * Hq + (size_t)it.kvh * G + gq) * D;
 #pragma unroll
             for (int h = 0; h < D / 32; ++h) {
                 uint32_t o[32];
                 tmem_ld32(t_o + h * 32, o);                  // warp-wide: padded rows join the load
-                if (R < it.rows) {
+                if (kSplit && it.piece) {
+                    float4* po = part_dims<D>(p.part_o, part) + h * 8 * kRows;   // a warp's rows side by side
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        po[c * kRows] = make_float4(__uint_as_float(o[4 * c]) * inv, __uint_as_float(o[4 * c + 1]) * inv,
+                                            __uint_as_float(o[4 * c + 2]) * inv, __uint_as_float(o[4 * c + 3]) * inv);
+                } else if (R < it.rows) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint4 w;
@@ -729,6 +853,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after_sync();
         tmem_dealloc(tmem, C::kTmemCols);
     }
+}
+
+// The pieces of a cut item, joined: M = max lse, w = 2^(lse - M), out = sum w o / sum w.  CTA (x, y): some
+// rows of the item that CTA x + 1 was the second to hold some of, if there is one; a warp: 8 rows, 16 dims.
+constexpr int kMergeThreads = 512;
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) wide_merge_kernel(const PrefillParams p) {
+    constexpr int kLanes = D / 4, kMergeRows = kMergeThreads / kLanes;
+    wait_prerequisite();
+    const int i = blockIdx.x + 1;
+    const int4 cut = p.cuts[i];
+    const int pieces = cut.x, b = cut.y, kvh = cut.z;
+    if (pieces < 2) return;
+    constexpr int kQuads = D / 16;                           // 16-dim columns of warps
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = blockIdx.y * kMergeRows + warp / kQuads * 8 + (lane >> 2), d4 = warp % kQuads * 4 + (lane & 3);
+    const int R = cut.w + row, q0 = p.cu_q[b], Tq = p.cu_q[b + 1] - q0;
+    if (R >= Tq * p.group) return;
+    float M = -FLT_MAX, W = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < pieces; ++k) {
+        const size_t part = (size_t)(k == 0 ? 2 * i - 1 : 2 * (i - 1 + k)) * kItemRows + row;
+        const float lse = p.part_lse[part];
+        if (lse == -FLT_MAX) continue;                       // nothing of it for this row
+        const float4 o = part_dims<D>(p.part_o, part)[d4 * kRows];
+        const float mn = fmaxf(M, lse), a = fast_exp2(M - mn), w = fast_exp2(lse - mn);
+        M = mn;
+        W = W * a + w;
+        acc.x = acc.x * a + w * o.x;
+        acc.y = acc.y * a + w * o.y;
+        acc.z = acc.z * a + w * o.z;
+        acc.w = acc.w * a + w * o.w;
+    }
+    const float inv = 1.f / W;
+    const int tok = R / p.group;
+    *reinterpret_cast<uint2*>(p.out + ((size_t)(q0 + tok) * p.num_q_heads + (size_t)kvh * p.group + (R - tok * p.group)) * D + d4 * 4) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -765,10 +926,10 @@ bool wide_pool_map(CUtensorMap* map, const void* base, const PrefillParams& p) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool kE2m1, bool kCausal>
-cudaError_t launch_w(const PrefillParams& p, int max_q_len, cudaStream_t stream) {
+template <int D, bool kE2m1, bool kCausal, bool kSplit>
+cudaError_t launch_wide(const PrefillParams& p, int max_q_len, cudaStream_t stream) {
     constexpr size_t smem = PCfg<D>::kSmem;
-    const auto kernel = prefill_wide_kernel<D, kE2m1, kCausal>;
+    const auto kernel = prefill_wide_kernel<D, kE2m1, kCausal, kSplit>;
     static std::atomic<uint64_t> attr_set{0};               // one bit per device
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -789,25 +950,65 @@ cudaError_t launch_w(const PrefillParams& p, int max_q_len, cudaStream_t stream)
     memset(&km, 0, sizeof km);
     memset(&vm, 0, sizeof vm);
     if (!kE2m1 && (!wide_pool_map(&km, p.k_cache, p) || !wide_pool_map(&vm, p.v_cache, p))) return cudaErrorInvalidValue;
-    kernel<<<(unsigned)std::min<long long>(items, sms), kThreads, smem, stream>>>(p, km, vm);
-    return cudaGetLastError();
+    const unsigned grid = (unsigned)(kSplit ? sms : std::min<long long>(items, sms));
+    kernel<<<grid, kThreads, smem, stream>>>(p, km, vm);
+    const cudaError_t e = cudaGetLastError();
+    if constexpr (!kSplit) {
+        return e;
+    } else {
+        if (e != cudaSuccess || grid < 2) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(grid - 1, kItemRows * (D / 4) / kMergeThreads);
+        cfg.blockDim = dim3(kMergeThreads);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, wide_merge_kernel<D>, p);
+    }
 }
 
 }  // namespace
 
+// Whether the last round's items of a 4-bit prefill are cut, as far as the call's bounds tell: the tiles that
+// it would take whole, less those of an even share, against the pieces' way through memory and the merge.
+// Measured (us, cut | whole; tiles saved), the last rows of contexts of the given length: 32 and 8 heads of 64,
+// 300 of 20000 tokens 114 | 329 (115), 512 of 3000 51 | 64 (14), 4 x 256 of 4000 95 | 76 (4), 4000 of 4000
+// 154 | 131 (2); 64 and 8 heads of 128, where the cut's registers are taken from the softmax's, 300 of 20000
+// 298 | 364 (72), 1021 of 15000 627 | 627 (32), 4 x 256 of 4000 207 | 186 (9).
+int wide_split_ctas(int32_t num_seqs, int32_t num_kv_heads, int32_t group, int32_t head_dim, int32_t max_q_len,
+                    int64_t max_len) {
+    int sms = 0;
+    if (num_sms_current_device(&sms) != PA_OK || sms < 2 || num_seqs < 1 || max_q_len < 1) return 0;
+    const int64_t nsh = (int64_t)num_seqs * num_kv_heads, rows = (int64_t)max_q_len * group;
+    const int64_t items = nsh * ((rows + kItemRows - 1) / kItemRows), last = items % sms;
+    // row tiles of a sequence that come before those of the last round end behind them
+    const int64_t seen = max_len - (items - last) / nsh * kItemRows / group;
+    const int64_t nt = seen > 0 ? (seen + kKeys - 1) / kKeys : 0;
+    const bool cut = last > 0 && items / sms < INT32_MAX && nt * (sms - last) >= (head_dim == 64 ? 12 : 40) * sms;
+    return cut ? sms : 0;
+}
+size_t wide_split_rows(int ctas) { return (size_t)ctas * 2 * kItemRows; }
+
 cudaError_t launch_prefill_e2m1(const PrefillParams& p, int max_q_len, cudaStream_t stream) {
-    if (p.head_dim == 64) return launch_w<64, true, true>(p, max_q_len, stream);
-    if (p.head_dim == 128) return launch_w<128, true, true>(p, max_q_len, stream);
+    if (p.head_dim == 64)
+        return p.cuts ? launch_wide<64, true, true, true>(p, max_q_len, stream)
+                      : launch_wide<64, true, true, false>(p, max_q_len, stream);
+    if (p.head_dim == 128)
+        return p.cuts ? launch_wide<128, true, true, true>(p, max_q_len, stream)
+                      : launch_wide<128, true, true, false>(p, max_q_len, stream);
     return cudaErrorInvalidValue;
 }
 
 // Cross attention.  With 128 dims these tiles; with 64 dims those of prefill_ws.cu, two CTAs an SM of
 // 128 rows each.  Measured (us, these | prefill_ws.cu), 16 heads: 8 x 448 rows over 1500 tokens, 128
 // dims 67 | 122, 64 dims 59 | 55; 32 x 100 over 500, 128 dims 49 | 52, 64 dims 42 | 25; 32 and 8 heads,
-// 4 x 1024 over 4096, 128 dims 284 (967 TFLOP/s) | 505, 64 dims 264 | 241.  A call of few items (p.cuts)
-// goes to the stream of key tiles there.
+// 4 x 1024 over 4096, 128 dims 284 (967 TFLOP/s) | 505, 64 dims 264 | 241.  A call of few items
+// (p.cuts) goes to the stream of key tiles there.
 cudaError_t launch_cross(const PrefillParams& p, int max_q_len, cudaStream_t stream) {
-    if (p.head_dim == 128 && !p.cuts) return launch_w<128, false, false>(p, max_q_len, stream);
+    if (p.head_dim == 128 && !p.cuts) return launch_wide<128, false, false, false>(p, max_q_len, stream);
     return launch_cross_ws(p, max_q_len, stream);
 }
 

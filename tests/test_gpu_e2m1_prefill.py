@@ -134,6 +134,52 @@ def test_either_kernel(h, kernel, hq, hkv, d, bs):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("lens,rows,hq,hkv,d,bs", [
+    ([9000], [300], 8, 2, 64, 16),                        # few items, many pieces each
+    ([5000, 9900, 100, 6000, 0], [60, 200, 100, 1, 0], 16, 1, 128, 64),   # ragged, short ones among them
+    ([2600], [2600], 2, 2, 64, 16),                       # pieces behind a row's (or a row tile's) last key
+    ([6300], [6300], 1, 1, 128, 16),
+    ([2700, 130], [2690, 130], 1, 1, 64, 8),
+    ([1300, 1290, 40, 1200, 9, 1, 3500, 1280], [3, 7, 0, 2, 9, 1, 1280, 4], 4, 4, 64, 32),   # whole rounds before
+    ([1300, 1290, 40, 1200, 9, 1, 7000, 1280], [3, 7, 0, 2, 9, 1, 1280, 4], 4, 4, 128, 32),
+])
+def test_last_round_cut_between_ctas(h, lens, rows, hq, hkv, d, bs):
+    c = _case(len(lens) + hq + d, lens, rows, hq, hkv, d, bs, gs=(0.6, 2.3))
+    c.kernel = pa.PA_PREFILL_TCGEN05_WS
+    assert pa.pa_prefill_workspace_size(len(rows), max(rows), max(lens), c.desc, _options(c)) > 256
+    _check(c, h)
+    _check(c, h)
+
+
+@pytest.mark.gpu
+def test_cut_calls_report_and_repeat(h):
+    c = _case(31, [4000, 3500, 3900], [140, 150, 130], 8, 4, 64, 16)
+    c.kernel = pa.PA_PREFILL_TCGEN05_WS
+    ref, tol = _reference(c)
+    live = np.r_[0:140, 290:420]
+    keep, c.lens[1] = c.lens[1], 149
+    got, st = _run(c, h, longest=4000)
+    c.lens[1] = keep
+    assert st == -8 and (got[140:290] == 9.0).all() and np.all(np.abs(got - ref)[live] <= tol[live])
+    keep, c.tables[1, 3] = c.tables[1, 3], c.n
+    got, st = _run(c, h)
+    c.tables[1, 3] = keep
+    assert st == -7 and np.all(np.abs(got - ref)[live] <= tol[live])
+    x = _device(c, h)                                     # back to back in a graph, over one workspace
+    longest, ws = _workspace(c, max(c.rows), h)
+    outs = [torch.zeros_like(x[0]) for _ in range(2)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for out in outs * 3:
+            pa.pa_prefill_ex(*x, max(c.rows), longest, c.scale, out, ws, c.desc, _options(c))
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(*outs) and pa.pa_decode_status(ws) == 0
+    assert np.all(np.abs(outs[0].double().cpu().numpy() - ref) <= tol)
+
+
+@pytest.mark.gpu
 def test_long_and_many(h):
     _check(_case(3, [9000], [300], 8, 2, 64, 16), h)
     _check(_case(4, [20000, 1], [7, 1], 8, 1, 128, 16), h)
