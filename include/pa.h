@@ -373,7 +373,8 @@ PA_API int pa_prefill(const pa_bf16* q, const pa_bf16* k_cache, const pa_bf16* v
  * rows; PA_PREFILL_ROWS: the decode kernel with several rows' heads for its columns, Hq / Hkv <= 16;
  * PA_PREFILL_AUTO: the latter for few rows).
  * 4-bit K is widened to bf16 (rows: f16, as q is after a power of two per row) and V to f16
- * exactly, P is rounded to f16.  max_context_len: an upper bound of every context_lens[b] (a longer
+ * exactly, P is rounded to f16.  A NaN held in V may also reach rows before its token (P is 0
+ * there, and 0 NaN a NaN).  max_context_len: an upper bound of every context_lens[b] (a longer
  * sequence may be reported as a bad length).  workspace: pa_prefill_workspace_size bytes,
  * 256-byte aligned, zero-filled before its first use, one per call in flight.  The rest, and
  * the errors, as for pa_prefill; also PA_ERR_UNSUPPORTED for PA_KV_E4M3.
@@ -407,7 +408,8 @@ PA_API int pa_prefill_ex(const void* q, const void* k_cache, const void* v_cache
  * cu_seqlens_q as for pa_prefill; NULL (with max_q_len == 1): one query row a sequence, the
  * decoding step, which runs the decode kernels (shapes as for pa_decode) and is the form to use
  * there.  max_q_len >= every row count; max_encoder_len >= every encoder length (a longer one is
- * clipped to it by the NULL form; else it only chooses how the work is shared out).  workspace: pa_cross_attention_workspace_size bytes, 256-byte aligned,
+ * clipped to it by the NULL form; else it only chooses how the work is shared out).
+ * workspace: pa_cross_attention_workspace_size bytes (needs a current CUDA device), 256-byte aligned,
  * zero-filled before its first use, one per call in flight; its status word as for pa_decode
  * (more rows than max_q_len, or a length below zero or past the table: that sequence's rows are
  * left unwritten, or for the NULL form the length clipped, and pa_decode_status reports it).

@@ -19,14 +19,6 @@
 namespace pa {
 namespace {
 
-// One CTA of PG * D/4 threads per (sequence, kv head, query head): PG groups over
-// the pieces (piece k goes to group k % PG) times D/4 float4 columns of the head
-// dimension.  Each thread folds its pieces into a running (max, weight, sum)
-// state as their lse and output arrive (independent loads), and the groups'
-// states are merged the same way through shared memory.  Long contexts cut a
-// sequence into many pieces: 16 groups keep each thread's chain short there.
-// kStream: the stream partition's pieces (read from the sequence's descriptor);
-// else the split kernels' fixed splits.
 // Output row of column h (of p.cols) of kv head kvh: query head h of sequence b, or with few-row
 // prefill the (token, head) pair of it; -1 for a token that the sequence does not have.
 __device__ __forceinline__ int64_t merge_out_row(const DecodeParams& p, int32_t b, int32_t kvh, int32_t h) {
@@ -38,6 +30,14 @@ __device__ __forceinline__ int64_t merge_out_row(const DecodeParams& p, int32_t 
     return (int64_t)(row0 + tok) * p.num_q_heads + (int64_t)kvh * p.group + (h - tok * p.group);
 }
 
+// One CTA of PG * D/4 threads per (sequence, kv head, query head): PG groups over
+// the pieces (piece k goes to group k % PG) times D/4 float4 columns of the head
+// dimension.  Each thread folds its pieces into a running (max, weight, sum)
+// state as their lse and output arrive (independent loads), and the groups'
+// states are merged the same way through shared memory.  Long contexts cut a
+// sequence into many pieces: 16 groups keep each thread's chain short there.
+// kStream: the stream partition's pieces (read from the sequence's descriptor);
+// else the split kernels' fixed splits.
 template <int D, bool kStream, int PG>
 __global__ void __launch_bounds__(PG * D / 4) merge_kernel(const DecodeParams p) {
     constexpr int kCols = D / 4;
