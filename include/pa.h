@@ -386,8 +386,8 @@ typedef struct pa_prefill_options {
     float v_scale;       /* PA_KV_E2M1: scale of the V cache tensor (> 0)                     */
 } pa_prefill_options;
 
-/* Bytes of workspace pa_prefill_ex needs for these arguments (0 on bad ones; needs a current CUDA
- * device for 4-bit pools). */
+/* Bytes of workspace pa_prefill_ex needs for these arguments, and for every call of fewer sequences, fewer
+ * rows or shorter contexts (0 on bad arguments; needs a current CUDA device for 4-bit pools). */
 PA_API size_t pa_prefill_workspace_size(int32_t num_seqs, int32_t max_q_len, int32_t max_context_len,
                                         const pa_cache_desc* desc, const pa_prefill_options* options);
 PA_API int pa_prefill_ex(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
@@ -409,7 +409,8 @@ PA_API int pa_prefill_ex(const void* q, const void* k_cache, const void* v_cache
  * decoding step, which runs the decode kernels (shapes as for pa_decode) and is the form to use
  * there.  max_q_len >= every row count; max_encoder_len >= every encoder length (a longer one is
  * clipped to it by the NULL form; else it only chooses how the work is shared out).
- * workspace: pa_cross_attention_workspace_size bytes (needs a current CUDA device), 256-byte aligned,
+ * workspace: pa_cross_attention_workspace_size bytes (needs a current CUDA device; the NULL form: of its
+ * arguments, else: of these or larger ones), 256-byte aligned,
  * zero-filled before its first use, one per call in flight; its status word as for pa_decode
  * (more rows than max_q_len, or a length below zero or past the table: that sequence's rows are
  * left unwritten, or for the NULL form the length clipped, and pa_decode_status reports it).

@@ -617,22 +617,43 @@ struct RowsPlan {
     size_t off_lse, off_o, bytes;
 };
 
-static bool rows_plan(int32_t num_seqs, int32_t max_q_len, const pa_cache_desc& d, RowsPlan* r) {
-    const int32_t G = d.num_q_heads / d.num_kv_heads;
-    if (G > 16 || max_q_len < 1 || (int64_t)num_seqs * ceil_div(max_q_len, 16 / G) > INT32_MAX / 2) return false;
-    r->tokens = 16 / G < max_q_len ? 16 / G : max_q_len;
-    r->chunks = (max_q_len + r->tokens - 1) / r->tokens;
-    r->cols = r->tokens * G;
+static bool rows_plan_of(int32_t tokens, int32_t chunks, int64_t seqs, const pa_cache_desc& d, RowsPlan* r) {
+    r->tokens = tokens;
+    r->chunks = chunks;
+    r->cols = tokens * (d.num_q_heads / d.num_kv_heads);
     r->grid = e2m1_kernel_grid(d, r->cols, 0);
     if (r->grid <= 0) return false;
     r->desc_heads = e2m1_head_group(d.num_kv_heads);
     r->slices = r->grid * (8 / r->desc_heads);
     auto up = [](size_t x) { return (x + kWorkspaceAlign - 1) / kWorkspaceAlign * kWorkspaceAlign; };
     const size_t rows = (size_t)r->slices * 2 * d.num_kv_heads * r->cols;
-    r->off_lse = kWorkspaceAlign + up((size_t)(d.num_kv_heads / r->desc_heads) * num_seqs * r->chunks * 16);
+    r->off_lse = kWorkspaceAlign + up((size_t)(d.num_kv_heads / r->desc_heads) * seqs * 16);
     r->off_o = r->off_lse + up(rows * sizeof(float));
     r->bytes = r->off_o + up(rows * (size_t)d.head_dim * sizeof(float));
     return true;
+}
+static bool rows_plan(int32_t num_seqs, int32_t max_q_len, const pa_cache_desc& d, RowsPlan* r) {
+    const int32_t G = d.num_q_heads / d.num_kv_heads;
+    if (G > 16 || max_q_len < 1 || num_seqs * ceil_div(max_q_len, 16 / G) > INT32_MAX / 2) return false;
+    const int32_t tokens = std::min(16 / G, max_q_len), chunks = (int32_t)ceil_div(max_q_len, tokens);
+    return rows_plan_of(tokens, chunks, (int64_t)num_seqs * chunks, d, r);
+}
+// Bytes that no call of at most so many sequences and rows passes (0: none can run).  An automatic call takes
+// this kernel only where its chunks number at most 4 num_seqs + 3 SMs (rows_pay).
+static size_t rows_bytes(int32_t num_seqs, int32_t max_q_len, bool automatic, const pa_cache_desc& d) {
+    const int32_t G = d.num_q_heads / d.num_kv_heads;
+    int sms = 0;
+    if (G > 16 || num_seqs < 1 || max_q_len < 1 || num_sms_current_device(&sms) != PA_OK) return 0;
+    int64_t seqs = num_seqs * ceil_div(max_q_len, 16 / G);
+    if (automatic) seqs = std::min<int64_t>(seqs, 4 * (int64_t)num_seqs + 3 * sms);
+    if (seqs > INT32_MAX / 2) return 0;
+    size_t most = 0;
+    for (int32_t t = std::min(16 / G, max_q_len); t > 0; --t) {
+        RowsPlan r;
+        if (!rows_plan_of(t, 1, seqs, d, &r)) return 0;
+        most = std::max(most, r.bytes);
+    }
+    return most;
 }
 
 // Whether an automatic call of this shape takes it.  The rows' kernel reads and widens the keys once per
@@ -672,6 +693,10 @@ static CutPlan cut_plan(int ctas, size_t rows, int32_t head_dim) {
     c.bytes = c.off_o + rows * head_dim * sizeof(float);
     return c;
 }
+// Whether any call of contexts up to max_len cuts items, where less than `tiles` of `keys` keys do not pay.
+static bool may_cut(int64_t max_len, const pa_cache_desc& d, int keys, int tiles) {
+    return ceil_div(std::min<int64_t>(max_len, (int64_t)d.max_blocks_per_seq * d.block_size), keys) >= tiles;
+}
 static CutPlan prefill_plan(int32_t num_seqs, int32_t max_q_len, int32_t max_len, const pa_cache_desc& d) {
     const int64_t held = std::min<int64_t>(max_len, (int64_t)d.max_blocks_per_seq * d.block_size);
     const int ctas = wide_split_ctas(num_seqs, d.num_kv_heads, d.num_q_heads / d.num_kv_heads, d.head_dim,
@@ -697,15 +722,19 @@ extern "C" size_t pa_prefill_workspace_size(int32_t num_seqs, int32_t max_q_len,
     if (check_desc(desc) != PA_OK || num_seqs < 0 || max_q_len < 0 || max_context_len < 0 ||
         check_prefill_options(options) != PA_OK)
         return 0;
-    if (options && options->kv_dtype == PA_KV_E2M1 &&
-        (options->kernel == PA_PREFILL_ROWS || (options->kernel == PA_PREFILL_AUTO && rows_pay(num_seqs, max_q_len, *desc)))) {
-        RowsPlan r;
-        if (check_e2m1_desc(desc) != PA_OK) return 0;
-        if (max_q_len > 0 && num_seqs > 0) return rows_plan(num_seqs, max_q_len, *desc, &r) ? r.bytes : 0;
-    } else if (options && options->kv_dtype == PA_KV_E2M1) {
-        return prefill_plan(num_seqs, max_q_len, max_context_len, *desc).bytes;
+    size_t bytes = kWorkspaceAlign;
+    if (options && options->kv_dtype == PA_KV_E2M1 && num_seqs > 0 && max_q_len > 0) {
+        int sms = 0;
+        if (check_e2m1_desc(desc) != PA_OK || num_sms_current_device(&sms) != PA_OK) return 0;
+        if (options->kernel != PA_PREFILL_TCGEN05_WS) {
+            const size_t rows = rows_bytes(num_seqs, max_q_len, options->kernel == PA_PREFILL_AUTO, *desc);
+            if (rows == 0 && options->kernel == PA_PREFILL_ROWS) return 0;
+            bytes = std::max(bytes, rows);
+        }
+        if (options->kernel != PA_PREFILL_ROWS && may_cut(max_context_len, *desc, 128, wide_split_tiles(desc->head_dim)))
+            bytes = std::max(bytes, cut_plan(sms, wide_split_rows(sms), desc->head_dim).bytes);
     }
-    return kWorkspaceAlign;
+    return bytes;
 }
 
 extern "C" int pa_prefill_ex(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
@@ -805,8 +834,16 @@ static CutPlan cross_plan(int32_t num_seqs, int32_t max_q_len, int32_t max_len, 
 extern "C" size_t pa_cross_attention_workspace_size(int32_t num_seqs, int32_t max_q_len, int32_t max_encoder_len,
                                                     const pa_cache_desc* desc) {
     if (check_desc(desc) != PA_OK || num_seqs < 0 || max_q_len < 0 || max_encoder_len < 0) return 0;
-    const size_t step = max_q_len == 1 ? pa_decode_workspace_size(num_seqs, max_encoder_len, desc) : 0;
-    return std::max(step, cross_plan(num_seqs, max_q_len, max_encoder_len, *desc).bytes);
+    if (num_seqs == 0 || max_q_len == 0) return kWorkspaceAlign;
+    // the NULL form of this shape, and a cut call of any smaller one
+    size_t bytes = kWorkspaceAlign;
+    if (max_q_len == 1) bytes = std::max(bytes, pa_decode_workspace_size(num_seqs, max_encoder_len, desc));
+    if ((desc->head_dim == 64 || desc->head_dim == 128) && may_cut(max_encoder_len, *desc, 64, cross_ws_tiles(desc->head_dim))) {
+        const int slices = cross_ws_resident(desc->head_dim);
+        if (slices == 0) return 0;
+        bytes = std::max(bytes, cut_plan(slices, (size_t)slices * 2 * 128, desc->head_dim).bytes);
+    }
+    return bytes;
 }
 
 extern "C" int pa_cross_attention(const pa_bf16* q, const pa_bf16* k_cache, const pa_bf16* v_cache,

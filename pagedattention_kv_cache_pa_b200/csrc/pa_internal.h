@@ -106,10 +106,13 @@ cudaError_t launch_prefill_tc(const PrefillParams& p, int max_q_len, cudaStream_
 cudaError_t launch_prefill_ws(const PrefillParams& p, int max_q_len, cudaStream_t stream);
 // cross attention: either kernel's tiles without the causal mask
 cudaError_t launch_cross_ws(const PrefillParams& p, int max_q_len, cudaStream_t stream);
+int cross_ws_resident(int head_dim);           // CTAs at once (0: no device): most slices of any call
+constexpr int cross_ws_tiles(int head_dim) { return head_dim == 64 ? 16 : 12; }   // see cross_ws_slices
 int cross_ws_slices(int32_t num_seqs, int32_t num_kv_heads, int32_t group, int32_t head_dim,
                     int32_t max_q_len, int64_t max_len);
 cudaError_t launch_cross(const PrefillParams& p, int max_q_len, cudaStream_t stream);
 // CTAs that share the last round's items of prefill_wide.cu (0: they are not cut), rows of partial states
+constexpr int wide_split_tiles(int head_dim) { return head_dim == 64 ? 12 : 40; }   // see wide_split_ctas
 int wide_split_ctas(int32_t num_seqs, int32_t num_kv_heads, int32_t group, int32_t head_dim, int32_t max_q_len,
                     int64_t max_len);
 size_t wide_split_rows(int ctas);

@@ -987,7 +987,7 @@ int wide_split_ctas(int32_t num_seqs, int32_t num_kv_heads, int32_t group, int32
     // row tiles of a sequence that come before those of the last round end behind them
     const int64_t seen = max_len - (items - last) / nsh * kItemRows / group;
     const int64_t nt = seen > 0 ? (seen + kKeys - 1) / kKeys : 0;
-    const bool cut = last > 0 && items / sms < INT32_MAX && nt * (sms - last) >= (head_dim == 64 ? 12 : 40) * sms;
+    const bool cut = last > 0 && items / sms < INT32_MAX && nt * (sms - last) >= wide_split_tiles(head_dim) * sms;
     return cut ? sms : 0;
 }
 size_t wide_split_rows(int ctas) { return (size_t)ctas * 2 * kItemRows; }

@@ -211,7 +211,7 @@ __device__ __forceinline__ CrossSeq cross_seq(const PrefillParams& p, int b) {
     c.q0 = p.cu_q[b];
     c.Tq = p.cu_q[b + 1] - c.q0;
     c.L = p.context_lens[b];
-    c.bad = c.Tq > 0 && (c.L < 0 || c.L > p.max_blocks_per_seq * p.block_size || c.Tq > p.max_q_len);
+    c.bad = c.Tq > 0 && (c.L < 0 || c.L > (long long)p.max_blocks_per_seq * p.block_size || c.Tq > p.max_q_len);
     c.row_tiles = c.Tq <= 0 || c.bad ? 0 : (c.Tq * p.group + kWsRows - 1) / kWsRows;
     c.nt = c.L > 0 ? (c.L - 1) / kWsKeys + 1 : 1;
     c.tiles = (long long)c.row_tiles * p.num_kv_heads * c.nt;
@@ -856,6 +856,12 @@ cudaError_t launch_prefill_ws(const PrefillParams& p, int max_q_len, cudaStream_
     return cudaErrorInvalidValue;
 }
 
+int cross_ws_resident(int head_dim) {
+    int sms = 0;
+    if (num_sms_current_device(&sms) != PA_OK) return 0;
+    return sms * (head_dim == 64 ? WsCfg<64>::kMinBlocks : WsCfg<128>::kMinBlocks);
+}
+
 // Slices of the stream of a cross attention call (the workspace holds two partial states of 128 rows
 // each), or 0 where whole items to a CTA are the better way.  A stream saves an item's CTA the tiles that
 // idle ones take, and costs the states' way through memory and the merge: about 16 tiles' time with 64 dims,
@@ -866,13 +872,11 @@ cudaError_t launch_prefill_ws(const PrefillParams& p, int max_q_len, cudaStream_
 // CTAs of the last round are no loss: two CTAs an SM slow one another.)
 int cross_ws_slices(int32_t num_seqs, int32_t num_kv_heads, int32_t group, int32_t head_dim, int32_t max_q_len,
                     int64_t max_len) {
-    int sms = 0;
-    if (num_sms_current_device(&sms) != PA_OK) return 0;
-    const int64_t resident = (int64_t)sms * (head_dim == 64 ? WsCfg<64>::kMinBlocks : WsCfg<128>::kMinBlocks);
+    const int64_t resident = cross_ws_resident(head_dim);
     const int64_t row_tiles = ((int64_t)max_q_len * group + kWsRows - 1) / kWsRows;
     if ((int64_t)num_seqs * num_kv_heads >= resident || row_tiles >= resident) return 0;
     const int64_t items = (int64_t)num_seqs * num_kv_heads * row_tiles;
-    return items < resident && (max_len + kWsKeys - 1) / kWsKeys * (resident - items) >= (head_dim == 64 ? 16 : 12) * resident
+    return items < resident && (max_len + kWsKeys - 1) / kWsKeys * (resident - items) >= cross_ws_tiles(head_dim) * resident
                ? (int)resident : 0;
 }
 

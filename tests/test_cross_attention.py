@@ -36,5 +36,5 @@ def test_refusals():
 
 
 def test_workspace_size_of_many_rows():
-    assert pa.pa_cross_attention_workspace_size(3, 5, 100, _desc()) == 256
+    assert pa.pa_cross_attention_workspace_size(3, 5, 100, _desc()) >= 256
     assert binding.lib.pa_cross_attention_workspace_size(-1, 5, 100, ctypes.byref(_desc())) == 0

@@ -234,6 +234,37 @@ def test_graph_streams_and_repeats(h, rows):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 64), (16, 1, 128), (7, 7, 64), (10, 2, 128)])
+@pytest.mark.parametrize("kernel", [pa.PA_PREFILL_AUTO, pa.PA_PREFILL_ROWS, pa.PA_PREFILL_TCGEN05_WS])
+def test_a_workspace_serves_smaller_calls(h, hq, hkv, d, kernel):
+    rng = np.random.default_rng(hq + kernel)
+    desc = _desc(num_q_heads=hq, num_kv_heads=hkv, head_dim=d, max_blocks_per_seq=4000)
+    opt = pa.PrefillOptions(kernel=kernel, kv_dtype=pa.PA_KV_E2M1, k_scale=1.0, v_scale=1.0)
+    most = (40, 1500, 50000)
+    size = pa.pa_prefill_workspace_size(*most, desc, opt)
+    cross = pa.pa_cross_attention_workspace_size(*most, desc)
+    for _ in range(40):
+        small = [int(np.exp(rng.uniform(0, np.log(m)))) for m in most]
+        assert pa.pa_prefill_workspace_size(*small, desc, opt) <= size
+        small[1] = max(2, small[1])                       # (one row a sequence without offsets has the decode's size)
+        assert pa.pa_cross_attention_workspace_size(*small, desc) <= cross
+
+
+@pytest.mark.gpu
+def test_one_workspace_for_calls_of_every_path(h):
+    cs = [_case(41, [700, 4000], [3, 1], 16, 4, 64, 16), _case(42, [5000], [300], 16, 4, 64, 16),
+          _case(43, [900, 20, 600], [400, 20, 300], 16, 4, 64, 16)]
+    size = max(pa.pa_prefill_workspace_size(3, 400, 5000, c.desc, _options(c)) for c in cs)
+    ws = torch.zeros(size, dtype=torch.uint8, device=h.DEV)
+    for c in cs * 2:
+        args = _device(c, h)
+        out = torch.zeros_like(args[0])
+        pa.pa_prefill_ex(*args, max(c.rows), int(c.lens.max()), c.scale, out, ws, c.desc, _options(c))
+        ref, tol = _reference(c)
+        assert pa.pa_decode_status(ws) == 0 and np.all(np.abs(out.double().cpu().numpy() - ref) <= tol)
+
+
+@pytest.mark.gpu
 def test_bf16_options_are_pa_prefill(h):
     rng = np.random.default_rng(2)
     from tests.test_gpu_e2m1 import normal
