@@ -87,12 +87,15 @@ __global__ void __launch_bounds__(kThreads) append_e2m1_kernel(const E2m1Args a,
 // tokens has few pairs beside its rows.  So the rows' threads form them for the first tile only,
 // with their first loads of q already under way; from then on a ninth warp forms the next tile's
 // while the others work on this one.  (Formed between two barriers by all, they were a third of the
-// time: 151 us for 16384 tokens of 64 + 2 x 8 heads of 128.)
+// time.)  Bound by the loads' latency and DRAM: 16384 tokens of 64 + 2 x 8 heads of 128 take, with their
+// read-back, 141 us (690 MB, 76 % of the copy rate) with three CTAs an SM of two rows in flight a thread, 144
+// with two CTAs of four, 154 with three of four or four of two (spills), 168 with the next tile's rows
+// requested into L2 ahead.
 constexpr int kMaxTokens = 8;
-constexpr int kRopeThreads = kThreads + 32;
+constexpr int kRopeThreads = kThreads + 32, kRopeCtas = 3;   // CTAs an SM
 
 template <int D, bool kAtEnd>
-__global__ void __launch_bounds__(kRopeThreads, 2)
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
     rope_append_e2m1_kernel(const E2m1Args a, const DecodeParams p, int tokens_per_cta) {
     allow_dependents();
     constexpr int kHalf = D / 2, kQItems = D / 16, kKItems = D / 32, kVItems = D / 16;
@@ -138,7 +141,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
         }
     };
     // q rows (token, head) are contiguous: kQItems threads a row, kAhead rows in flight a thread
-    constexpr int kRowStep = kThreads / kQItems, kAhead = 4;
+    constexpr int kRowStep = kThreads / kQItems, kAhead = 2;
     const int c8 = (tid % kQItems) * 8;
     uint4 x1[kAhead], x2[kAhead];
     auto load_q = [&](int64_t t0, int row, int rows) {
@@ -278,14 +281,14 @@ __global__ void __launch_bounds__(kThreads) gather_e2m1_kernel(const E2m1Args a,
     }
 }
 
-// Tokens a CTA takes at a time: up to `most`, few enough that a small call spreads over two CTAs an SM.
-int tokens_per_cta(int32_t T, int most) {
-    const int spread = (T + 295) / 296;
+// Tokens a CTA takes at a time: up to `most`, few enough that a small call spreads over `ctas` CTAs.
+int tokens_per_cta(int32_t T, int most, int ctas) {
+    const int spread = (T + ctas - 1) / ctas;
     return spread < most ? (spread < 1 ? 1 : spread) : most;
 }
 unsigned rope_grid(int32_t T, int tpc) {   // resident at once: a CTA's later tiles have their angles ready
     const int64_t g = ((int64_t)T + tpc - 1) / tpc;
-    return (unsigned)(g < 148 * 2 ? g : 148 * 2);
+    return (unsigned)(g < 148 * kRopeCtas ? g : 148 * kRopeCtas);
 }
 unsigned grid_for(int32_t T, int tpc) {
     const int64_t g = ((int64_t)T + tpc - 1) / tpc;
@@ -303,14 +306,14 @@ cudaError_t launch_append_e2m1(const pa_bf16* q, pa_bf16* q_out, const pa_bf16* 
                (int64_t)d.num_blocks * d.block_size, theta, k_inv, v_inv, k_cache, v_cache};
     const int D = d.head_dim;
     if (theta > 0.f) {
-        const int tpc = tokens_per_cta(T, kMaxTokens);
+        const int tpc = tokens_per_cta(T, kMaxTokens, 148 * kRopeCtas);
         const DecodeParams none{};
         if (D == 64)
             rope_append_e2m1_kernel<64, false><<<rope_grid(T, tpc), kRopeThreads, 0, stream>>>(a, none, tpc);
         else
             rope_append_e2m1_kernel<128, false><<<rope_grid(T, tpc), kRopeThreads, 0, stream>>>(a, none, tpc);
     } else {
-        const int tpc = tokens_per_cta(T, 8);
+        const int tpc = tokens_per_cta(T, 8, 296);
         if (D == 64)
             append_e2m1_kernel<64><<<grid_for(T, tpc), kThreads, 0, stream>>>(a, tpc);
         else
@@ -328,7 +331,7 @@ cudaError_t launch_append_e2m1_at_end(const DecodeParams& p, uint16_t* q_out, cu
                reinterpret_cast<uint8_t*>(const_cast<uint16_t*>(p.k_cache)),
                reinterpret_cast<uint8_t*>(const_cast<uint16_t*>(p.v_cache))};
     const int D = p.head_dim;
-    const int tpc = tokens_per_cta(p.num_seqs, kMaxTokens);
+    const int tpc = tokens_per_cta(p.num_seqs, kMaxTokens, 148 * kRopeCtas);
     if (D == 64)
         rope_append_e2m1_kernel<64, true><<<rope_grid(p.num_seqs, tpc), kRopeThreads, 0, stream>>>(a, p, tpc);
     else
@@ -343,7 +346,7 @@ cudaError_t launch_gather_e2m1(const uint8_t* k_cache, const uint8_t* v_cache, c
     E2m1Args a{nullptr, nullptr, nullptr, nullptr, nullptr, slots, T, d.num_q_heads, d.num_kv_heads, d.block_size,
                (int64_t)d.num_blocks * d.block_size, 0.f, k_scale, v_scale, const_cast<uint8_t*>(k_cache),
                const_cast<uint8_t*>(v_cache)};
-    const int tpc = tokens_per_cta(T, 8);
+    const int tpc = tokens_per_cta(T, 8, 296);
     if (d.head_dim == 64)
         gather_e2m1_kernel<64><<<grid_for(T, tpc), kThreads, 0, stream>>>(a, k, v, tpc);
     else
