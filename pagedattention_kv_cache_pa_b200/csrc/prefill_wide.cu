@@ -30,15 +30,17 @@
 //   warp 12         (of a fourth warpgroup) MMA issue: O += P(t) V(t) of a row tile, then its
 //                   S(t + 1), which with 128 dims overwrites P(t): MMAs of one shape run in order.
 //                   While one row tile's products run, the other's softmax has the exponential
-//                   unit to itself.
+//                   unit to itself; so that it is so from an item's start, the second row tile's
+//                   first scores wait for the first's P (153 -> 148 us and 630 -> 615 below).
 // K and V tiles have rings of their own.
 //
 // Long prefills of few items: the items of the last, unfilled round are cut (Walk, wide_split_ctas).
 //
-// Measured (a call inside a CUDA graph): 4-bit, 32 and 8 heads of 64, 4 x 2048 rows 153 us (450 TFLOP/s); 64 and
-// 8 heads of 128, the last 1021 rows of 15000 630 us (824 TFLOP/s, the exponentials alone 226 us); cross
+// Measured (a call inside a CUDA graph): 4-bit, 32 and 8 heads of 64, 4 x 2048 rows 148 us (465 TFLOP/s); 64 and
+// 8 heads of 128, the last 1021 rows of 15000 615 us (844 TFLOP/s, the exponentials alone 226 us); cross
 // attention, 32 and 8 heads of 128, 4 x 1024 rows over 4096 tokens 274 us (1000 TFLOP/s).  Bound by a row tile's
-// chain of scores, softmax and products: without the softmax's arithmetic the first two take 125 and 513 us.
+// chain of scores, softmax and products: without the softmax's arithmetic an earlier form of the first two took
+// 125 and 513 us.
 //
 // Every wait is bounded (2 s, then the timeout status bit); the tensor memory is freed and no
 // asynchronous operation is left when a CTA exits.
@@ -605,18 +607,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (__shfl_sync(0xffffffffu, kind, 0) != 1) continue;
                 const int n0 = __shfl_sync(0xffffffffu, it.nt[0], 0), n1 = __shfl_sync(0xffffffffu, it.nt[1], 0);
                 const int nt = max(n0, n1);
-                // the first scores of either row tile
+                // the first scores of either row tile; the second's wait for the first's P
+                const bool late = n0 > 0 && n1 > 0;
+                const int ks0 = ks;
                 if (!(ok = warp_wait(bar_kf + 8 * ks, (uint32_t)kph, p.status))) break;
 #pragma unroll
                 for (int gr = 0; gr < 2; ++gr) {
-                    if ((gr ? n1 : n0) == 0) continue;
+                    if ((gr ? n1 : n0) == 0 || (gr && late)) continue;
                     const int buf = items[gr] % QB;
                     if (!(ok = ok && warp_wait(bar_q(buf, gr), (uint32_t)((items[gr] / QB) & 1), p.status))) break;
                     tc_fence_after_sync();
                     issue_s(gr, buf, ks);
                 }
                 if (!ok) break;
-                if (leader) umma_commit(bar_ke + 8 * ks);
+                if (leader && !late) umma_commit(bar_ke + 8 * ks);
                 if (++ks == ST) ks = 0, kph ^= 1;
                 for (int t = 0; t < nt && ok; ++t) {
                     const bool more = t + 1 < nt;
@@ -631,6 +635,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (t == 0 && items[gr] > 0)
                             ok = ok && warp_wait(bar_of(gr), (uint32_t)((items[gr] - 1) & 1), p.status);
                         if (!ok) break;
+                        if (gr == 0 && t == 0 && late) {
+                            const int buf = items[1] % QB;
+                            if (!(ok = warp_wait(bar_q(buf, 1), (uint32_t)((items[1] / QB) & 1), p.status))) break;
+                            tc_fence_after_sync();
+                            issue_s(1, buf, ks0);
+                            if (leader) umma_commit(bar_ke + 8 * ks0);
+                        }
                         tc_fence_after_sync();
                         issue_o(gr, vs, t == 0);
                         if (t + 1 < n) issue_s(gr, items[gr] % QB, ks);
@@ -981,9 +992,9 @@ cudaError_t launch_wide(const PrefillParams& p, int max_q_len, cudaStream_t stre
 // Whether the last round's items of a 4-bit prefill are cut, as far as the call's bounds tell: the tiles that
 // it would take whole, less those of an even share, against the pieces' way through memory and the merge.
 // Measured (us, cut | whole; tiles saved), the last rows of contexts of the given length: 32 and 8 heads of 64,
-// 300 of 20000 tokens 114 | 329 (115), 512 of 3000 51 | 64 (14), 4 x 256 of 4000 95 | 76 (4), 4000 of 4000
-// 154 | 131 (2); 64 and 8 heads of 128, where the cut's registers are taken from the softmax's, 300 of 20000
-// 298 | 364 (72), 1021 of 15000 627 | 627 (32), 4 x 256 of 4000 207 | 186 (9).
+// 300 of 20000 tokens 113 | 316 (115), 512 of 3000 54 | 60 (14), 4 x 256 of 4000 95 | 73 (4), 4000 of 4000
+// 156 | 126 (2); 64 and 8 heads of 128, where the cut's registers are taken from the softmax's, 300 of 20000
+// 269 | 368 (72), 1021 of 15000 610 | 616 (32), 4 x 256 of 4000 212 | 182 (9).
 int wide_split_ctas(int32_t num_seqs, int32_t num_kv_heads, int32_t group, int32_t head_dim, int32_t max_q_len,
                     int64_t max_len) {
     int sms = 0;
