@@ -31,13 +31,13 @@
 //                   S(t + 1), which with 128 dims overwrites P(t): MMAs of one shape run in order.
 //                   While one row tile's products run, the other's softmax has the exponential
 //                   unit to itself; so that it is so from an item's start, the second row tile's
-//                   first scores wait for the first's P (153 -> 148 us and 630 -> 615 below).
+//                   first scores follow the first's second (153 -> 147 us and 630 -> 613 below).
 // K and V tiles have rings of their own.
 //
 // Long prefills of few items: the items of the last, unfilled round are cut (Walk, wide_split_ctas).
 //
-// Measured (a call inside a CUDA graph): 4-bit, 32 and 8 heads of 64, 4 x 2048 rows 148 us (465 TFLOP/s); 64 and
-// 8 heads of 128, the last 1021 rows of 15000 615 us (844 TFLOP/s, the exponentials alone 226 us); cross
+// Measured (a call inside a CUDA graph): 4-bit, 32 and 8 heads of 64, 4 x 2048 rows 147 us (467 TFLOP/s); 64 and
+// 8 heads of 128, the last 1021 rows of 15000 613 us (847 TFLOP/s, the exponentials alone 226 us); cross
 // attention, 32 and 8 heads of 128, 4 x 1024 rows over 4096 tokens 274 us (1000 TFLOP/s).  Bound by a row tile's
 // chain of scores, softmax and products: without the softmax's arithmetic an earlier form of the first two took
 // 125 and 513 us.
@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (__shfl_sync(0xffffffffu, kind, 0) != 1) continue;
                 const int n0 = __shfl_sync(0xffffffffu, it.nt[0], 0), n1 = __shfl_sync(0xffffffffu, it.nt[1], 0);
                 const int nt = max(n0, n1);
-                // the first scores of either row tile; the second's wait for the first's P
+                // the first scores of either row tile; the second's follow the first's second
                 const bool late = n0 > 0 && n1 > 0;
                 const int ks0 = ks;
                 if (!(ok = warp_wait(bar_kf + 8 * ks, (uint32_t)kph, p.status))) break;
@@ -635,6 +635,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (t == 0 && items[gr] > 0)
                             ok = ok && warp_wait(bar_of(gr), (uint32_t)((items[gr] - 1) & 1), p.status);
                         if (!ok) break;
+                        tc_fence_after_sync();
+                        issue_o(gr, vs, t == 0);
+                        if (t + 1 < n) issue_s(gr, items[gr] % QB, ks);
                         if (gr == 0 && t == 0 && late) {
                             const int buf = items[1] % QB;
                             if (!(ok = warp_wait(bar_q(buf, 1), (uint32_t)((items[1] / QB) & 1), p.status))) break;
@@ -642,9 +645,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                             issue_s(1, buf, ks0);
                             if (leader) umma_commit(bar_ke + 8 * ks0);
                         }
-                        tc_fence_after_sync();
-                        issue_o(gr, vs, t == 0);
-                        if (t + 1 < n) issue_s(gr, items[gr] % QB, ks);
                     }
                     if (!ok) break;
                     if (leader) {
@@ -994,7 +994,7 @@ cudaError_t launch_wide(const PrefillParams& p, int max_q_len, cudaStream_t stre
 // Measured (us, cut | whole; tiles saved), the last rows of contexts of the given length: 32 and 8 heads of 64,
 // 300 of 20000 tokens 113 | 316 (115), 512 of 3000 54 | 60 (14), 4 x 256 of 4000 95 | 73 (4), 4000 of 4000
 // 156 | 126 (2); 64 and 8 heads of 128, where the cut's registers are taken from the softmax's, 300 of 20000
-// 269 | 368 (72), 1021 of 15000 610 | 616 (32), 4 x 256 of 4000 212 | 182 (9).
+// 262 | 368 (72), 1021 of 15000 610 | 616 (32), 4 x 256 of 4000 212 | 182 (9).
 int wide_split_ctas(int32_t num_seqs, int32_t num_kv_heads, int32_t group, int32_t head_dim, int32_t max_q_len,
                     int64_t max_len) {
     int sms = 0;
