@@ -422,6 +422,39 @@ def test_append_decode(h, hq, hkv, d, bs, theta):
     assert np.array_equal(h.to_host_bits(q), q_before)
 
 
+@pytest.mark.parametrize("theta", [0.0, 10000.0], ids=["plain", "rope"])
+def test_append_decode_layers_started_early_in_a_graph(h, theta):
+    # layers of a step back to back over one workspace, each decode started early: the bits of plain calls
+    layers = [Case(91 + i, [700, 1, 33, 0, 1500], 32, 8, 64, 16) for i in range(3)]
+    rng = np.random.default_rng(6)
+    new = [(h.to_dev(normal(rng, 5, 8, 64)), h.to_dev(normal(rng, 5, 8, 64))) for _ in layers]
+    got = []
+    for flags in (0, pa.PA_FLAG_PDL):
+        opts = layers[0].options(flags=flags, rope_theta=theta)
+        ws = torch.zeros(pa.pa_decode_workspace_size(5, 1500, layers[0].desc, opts), dtype=torch.uint8, device=h.DEV)
+        held = [(h.to_dev(c.q), *kv, *(dev(x, h) for x in c.pools), dev(c.tables, h), dev(c.lens, h))
+                for c, kv in zip(layers, new)]
+        outs = [torch.zeros((5, 32, 64), dtype=torch.bfloat16, device=h.DEV) for _ in layers]
+        torch.cuda.synchronize()
+
+        def step():
+            for c, x, out in zip(layers, held, outs):
+                pa.pa_append_decode(*x, 1500, c.scale, out, ws, c.desc, opts)
+        if flags:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                step()
+            for _ in range(3):
+                g.replay()
+        else:
+            step()
+        torch.cuda.synchronize()
+        assert pa.pa_decode_status(ws) == 0
+        got.append(outs + [x for y in held for x in y[3:5]])
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+
+
 def test_serving_steps(h):
     """Prompts appended, then steps of one token a sequence with the block manager: the same tokens
     read back and attended to as the whole history quantized at once."""
