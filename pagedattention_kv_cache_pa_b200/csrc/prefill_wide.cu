@@ -28,7 +28,8 @@
 //                   exact too).  bf16: warp 8 requests TMA boxes of 64 dims x min(Bs, 64) tokens.
 //                   Rows of V past the sequence are zero, so P = 0 never meets a NaN there.
 //   warp 12         (of a fourth warpgroup) MMA issue: O += P(t) V(t) of a row tile, then its
-//                   S(t + 1), which with 128 dims overwrites P(t): MMAs of one shape run in order.
+//                   S(t + 1), which with 128 dims overwrites P(t) and so waits for those products: the
+//                   order of two MMAs is given for one accumulator and shape, and these have two.
 //                   While one row tile's products run, the other's softmax has the exponential
 //                   unit to itself; so that it is so from an item's start, the second row tile's
 //                   first scores follow the first's second (153 -> 147 us and 630 -> 613 below).
@@ -637,7 +638,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!ok) break;
                         tc_fence_after_sync();
                         issue_o(gr, vs, t == 0);
-                        if (t + 1 < n) issue_s(gr, items[gr] % QB, ks);
+                        if (t + 1 < n) {
+                            // P(t) lies in S(t + 1)'s columns: not before its products are done.  (An item's
+                            // first scores wait for its Q, published after the last item's products.)
+                            if (C::kOverS) {
+                                if (!(ok = warp_wait(bar_o(gr), (uint32_t)((tiles[gr] + t) & 1), p.status))) break;
+                                tc_fence_after_sync();
+                            }
+                            issue_s(gr, items[gr] % QB, ks);
+                        }
                         if (gr == 0 && t == 0 && late) {
                             const int buf = items[1] % QB;
                             if (!(ok = warp_wait(bar_q(buf, 1), (uint32_t)((items[1] / QB) & 1), p.status))) break;
