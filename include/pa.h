@@ -278,7 +278,9 @@ PA_API size_t pa_decode_workspace_size_ex(int32_t num_seqs, int32_t max_context_
  * options->kv_dtype == PA_KV_E2M1: the caches are 4-bit pools (see
  * pa_append_kv_e2m1), for any number of kv heads; kernel PA_KERNEL_AUTO or
  * PA_KERNEL_TENSOR (PA_ERR_UNSUPPORTED otherwise).  q is used as f16 after a
- * power of two per row, P as f16.  pa_append_decode quantizes the new rows as
+ * power of two per row, P as f16 after another: a weight is rounded by 2^-12 of
+ * itself down to 2^-25 of the largest score's, and by 2^-36 of that one's below.
+ * pa_append_decode quantizes the new rows as
  * pa_append_kv_e2m1 (pa_rope_append_kv_e2m1 with rope_theta > 0) does, in a
  * launch of its own before the decode.
  *
@@ -373,7 +375,8 @@ PA_API int pa_prefill(const pa_bf16* q, const pa_bf16* k_cache, const pa_bf16* v
  * rows; PA_PREFILL_ROWS: the decode kernel with several rows' heads for its columns, Hq / Hkv <= 16;
  * PA_PREFILL_AUTO: the latter for few rows).
  * 4-bit K is widened to bf16 (rows: f16, as q is after a power of two per row) and V to f16
- * exactly, P is rounded to f16.  A NaN held in V may also reach rows before its token (P is 0
+ * exactly, P is rounded to f16 as pa_decode's is (tiles: by 2^-12 down to 2^-21 of the row's largest
+ * weight, by 2^-32 of that below).  A NaN held in V may also reach rows before its token (P is 0
  * there, and 0 NaN a NaN).  max_context_len: an upper bound of every context_lens[b] (a longer
  * sequence may be reported as a bad length).  workspace: pa_prefill_workspace_size bytes,
  * 256-byte aligned, zero-filled before its first use, one per call in flight.  The rest, and

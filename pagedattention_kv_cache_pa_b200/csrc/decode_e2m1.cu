@@ -20,7 +20,7 @@
 //    group token by token for that).
 //  * Codes and scales multiply in f16, exactly: 2 x 4 significant bits, 2^-10 <= |code scale| <=
 //    2688.  q is brought to f16 by a power of two per row (its largest value near 2^8), undone on
-//    the scores; P is rounded to f16 (relative 2^-11), sums and outputs are fp32.
+//    the scores; P is rounded to f16 (see kHeadLog2), sums and outputs are fp32.
 //
 // The work is the concatenation, over groups of HG kv heads (HG = 8, 4, 2 or 1, the largest that
 // divides Hkv) and sequences, of slabs of tokens (an empty sequence counts one).  8 / HG teams of
@@ -48,7 +48,13 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr float kLazyLog2 = 8.f;      // a slab rescales O only when a score passes the max by this
+// P is rounded to f16, whose steps below 2^-14 no longer shrink with the value: a long context's many small
+// weights, which the sum keeps in fp32, would be lost from the products.  So the running max is kept 2^11
+// below the largest score (weights reach 2^11, and 2^15 before a rescale): a weight is rounded by 2^-12 of
+// itself down to 2^-25 of the largest, and by 2^-36 of the largest below that.
+constexpr float kHeadLog2 = 11.f;
+constexpr float kLazyLog2 = 4.f;      // a slab rescales O only when a score passes the largest by this
+static_assert(kHeadLog2 + kLazyLog2 < 16.f, "P in f16's range");
 
 template <int D, int NT>
 struct ECfg {
@@ -492,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-            need |= mx[nt][0] > m_run[nt][0] + kLazyLog2 || mx[nt][1] > m_run[nt][1] + kLazyLog2;
+            need |= mx[nt][0] > m_run[nt][0] + (kHeadLog2 + kLazyLog2) || mx[nt][1] > m_run[nt][1] + (kHeadLog2 + kLazyLog2);
         if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -501,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
                     float v = mx[nt][jj];
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-                    const float mn = fmaxf(m_run[nt][jj], v), al = fast_exp2(m_run[nt][jj] - mn);
+                    const float mn = fmaxf(m_run[nt][jj], v - kHeadLog2), al = fast_exp2(m_run[nt][jj] - mn);
                     m_run[nt][jj] = mn;
                     l_run[nt][jj] *= al;
 #pragma unroll

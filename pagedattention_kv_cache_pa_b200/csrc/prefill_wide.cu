@@ -73,7 +73,14 @@ constexpr int kThreads = 512;              // four warpgroups: softmax 0, softma
 // shares add up to the launch's: 2 x 168 + 120 + 56 = 4 x 128.
 constexpr int kLaunchRegs = 128, kSoftmaxRegs = 168, kLoadRegs = 120, kMmaRegs = 56;
 static_assert(2 * kSoftmaxRegs + kLoadRegs + kMmaRegs == 4 * kLaunchRegs, "register shares");
+// The running max stays kHeadLog2 below a row's largest score, and O is rescaled when a score passes that by
+// kRescaleLog2.  P in f16 (4-bit pools): weights up to 2^15, so that a long context's small ones are not lost (the
+// reason is in decode_e2m1.cu): rounded by 2^-12 of themselves down to 2^-21 of the row's largest, and by 2^-32
+// of the largest below that.  (11 and 4, as there, cost 10 to 20 % in rescales.)  In bf16 the range is fp32's.
 constexpr float kRescaleLog2 = 8.f;
+template <bool kE2m1>
+constexpr float kHeadLog2 = kE2m1 ? 7.f : 0.f;
+static_assert(kHeadLog2<true> + kRescaleLog2 < 16.f, "P in f16's range");
 
 template <int D>
 struct PCfg {
@@ -775,7 +782,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mq[(j >> 1) & 3] = fmax3(mq[(j >> 1) & 3], __uint_as_float(sr[j]), __uint_as_float(sr[j + 1]));
                 }
                 const float mx = fmax3(mq[0], mq[1], fmaxf(mq[2], mq[3]));
-                const float m_new = fmaxf(m_run, mx * sl2);  // finite: key 0 is in every row's range (pieces: above)
+                // finite: key 0 is in every row's range (pieces: above)
+                const float m_new = fmaxf(m_run, fmaf(mx, sl2, -kHeadLog2<kE2m1>));
                 if (t == 0) {
                     m_run = m_new;
                 } else {
