@@ -252,6 +252,36 @@ def _here(t, dtype_name: str, what: str, device: int, need: int = 0):
     return ptr
 
 
+def _sized(t, dtype_name: str, what: str, device, need: int):
+    """_here for a call over 4-bit pools; for the other types (device None) _dev."""
+    return _dev(t, dtype_name, what) if device is None else _here(t, dtype_name, what, device, need)
+
+
+def _decode_sizes(desc: "CacheDesc", options, n: int):
+    """(current device, elements of q and out, of a new K or V, of the tables) of a decode of n sequences
+    over 4-bit pools; (None, 0, 0, 0) over others."""
+    if options is None or options.kv_dtype != PA_KV_E2M1:
+        return None, 0, 0, 0
+    row = n * desc.head_dim
+    return _device(), row * desc.num_q_heads, row * desc.num_kv_heads, n * desc.max_blocks_per_seq
+
+
+def _scratch(t, device):
+    """Device pointer of a workspace of any type (or a raw int); over 4-bit pools it is of this device."""
+    if isinstance(t, int):
+        return t
+    if device is not None:
+        if t.get_device() != device:
+            raise ValueError("workspace is on %s, the current device is cuda:%d" % (t.device, device))
+        if not t.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+    return t.data_ptr()
+
+
+def _elements(t) -> int:
+    return 0 if t is None or isinstance(t, int) else t.numel()
+
+
 def _pool_elements(desc: "CacheDesc", kv_dtype: int) -> int:
     n = desc.num_blocks * desc.num_kv_heads * desc.block_size * desc.head_dim
     return n * 9 // 16 if kv_dtype == PA_KV_E2M1 else n
@@ -438,7 +468,10 @@ def pa_prefill_workspace_size(num_seqs: int, max_q_len: int, max_context_len: in
 def pa_prefill_ex(q, k_cache, v_cache, block_tables, cu_seqlens_q, context_lens, max_q_len: int, max_context_len: int,
                   scale: float, out, workspace, desc: CacheDesc, options: PrefillOptions | None = None,
                   stream=None) -> None:
-    """pa_prefill over a cache of the options' type (bf16, or 4-bit pools with their scales)."""
+    """pa_prefill over a cache of the options' type (bf16, or 4-bit pools with their scales).
+
+    q and out hold at least the rows that cu_seqlens_q counts (only the device knows how many), and out
+    all of q's."""
     n = int(context_lens.shape[0])
     kv_dtype = PA_KV_BF16 if options is None else options.kv_dtype
     at, pool, cache = _device(), _pool_elements(desc, kv_dtype), "bfloat16" if kv_dtype == PA_KV_BF16 else "uint8"
@@ -447,7 +480,8 @@ def pa_prefill_ex(q, k_cache, v_cache, block_tables, cu_seqlens_q, context_lens,
                              _here(block_tables, "int32", "block_tables", at, n * desc.max_blocks_per_seq),
                              _here(cu_seqlens_q, "int32", "cu_seqlens_q", at, n + 1),
                              _here(context_lens, "int32", "context_lens", at),
-                             n, int(max_q_len), int(max_context_len), float(scale), _here(out, "bfloat16", "out", at),
+                             n, int(max_q_len), int(max_context_len), float(scale),
+                             _here(out, "bfloat16", "out", at, _elements(q)),
                              _here(workspace, "uint8", "workspace", at), workspace.numel(), ctypes.byref(desc),
                              ctypes.byref(options) if options is not None else None, _stream(stream)), "pa_prefill_ex")
 
@@ -464,7 +498,8 @@ def pa_cross_attention(q, k_cache, v_cache, block_tables, cu_seqlens_q, encoder_
                        max_encoder_len: int, scale: float, out, workspace, desc: CacheDesc, stream=None) -> None:
     """Attention of each sequence's query rows to all of its encoder's tokens in the paged pool.
 
-    cu_seqlens_q: int32 [num_seqs + 1] row offsets, or None for one row a sequence (max_q_len 1)."""
+    cu_seqlens_q: int32 [num_seqs + 1] row offsets, or None for one row a sequence (max_q_len 1).  q and out
+    hold at least the rows that it counts, and out all of q's."""
     n = int(encoder_lens.shape[0])
     at, pool = _device(), _pool_elements(desc, PA_KV_BF16)
     rows = n * desc.num_q_heads * desc.head_dim if cu_seqlens_q is None else 0
@@ -473,7 +508,7 @@ def pa_cross_attention(q, k_cache, v_cache, block_tables, cu_seqlens_q, encoder_
                                   _here(block_tables, "int32", "block_tables", at, n * desc.max_blocks_per_seq),
                                   _here(cu_seqlens_q, "int32", "cu_seqlens_q", at, n + 1),
                                   _here(encoder_lens, "int32", "encoder_lens", at), n, int(max_q_len),
-                                  int(max_encoder_len), float(scale), _here(out, "bfloat16", "out", at, rows),
+                                  int(max_encoder_len), float(scale), _here(out, "bfloat16", "out", at, rows or _elements(q)),
                                   _here(workspace, "uint8", "workspace", at), workspace.numel(),
                                   ctypes.byref(desc), _stream(stream)), "pa_cross_attention")
 
@@ -509,12 +544,12 @@ def pa_decode(q, k_cache, v_cache, block_tables, context_lens, max_context_len: 
               num_seqs: int | None = None, workspace_bytes: int | None = None) -> None:
     n = int(context_lens.shape[0]) if num_seqs is None else int(num_seqs)
     wbytes = workspace.numel() * workspace.element_size() if workspace_bytes is None else int(workspace_bytes)
-    ws = workspace if isinstance(workspace, int) else workspace.data_ptr()
-    _check(lib.pa_decode_ex(_dev(q, "bfloat16", "q"), _cache(k_cache, desc, "k_cache", options),
+    at, rows, _, tables = _decode_sizes(desc, options, n)
+    _check(lib.pa_decode_ex(_sized(q, "bfloat16", "q", at, rows), _cache(k_cache, desc, "k_cache", options),
                             _cache(v_cache, desc, "v_cache", options),
-                            _dev(block_tables, "int32", "block_tables"),
-                            _dev(context_lens, "int32", "context_lens"), n, int(max_context_len),
-                            float(scale), _dev(out, "bfloat16", "out"), ws, wbytes,
+                            _sized(block_tables, "int32", "block_tables", at, tables),
+                            _sized(context_lens, "int32", "context_lens", at, n), n, int(max_context_len),
+                            float(scale), _sized(out, "bfloat16", "out", at, rows), _scratch(workspace, at), wbytes,
                             ctypes.byref(desc),
                             ctypes.byref(options) if options is not None else None,
                             _stream(stream)), "pa_decode")
@@ -527,14 +562,14 @@ def pa_append_decode(q, k, v, k_cache, v_cache, block_tables, context_lens, max_
     """Append each sequence's newest token at position context_lens-1, then decode."""
     n = int(context_lens.shape[0]) if num_seqs is None else int(num_seqs)
     wbytes = workspace.numel() * workspace.element_size() if workspace_bytes is None else int(workspace_bytes)
-    ws = workspace if isinstance(workspace, int) else workspace.data_ptr()
-    _check(lib.pa_append_decode(_dev(q, "bfloat16", "q"), _dev(k, "bfloat16", "k"),
-                                _dev(v, "bfloat16", "v"), _cache(k_cache, desc, "k_cache", options),
+    at, rows, new, tables = _decode_sizes(desc, options, n)
+    _check(lib.pa_append_decode(_sized(q, "bfloat16", "q", at, rows), _sized(k, "bfloat16", "k", at, new),
+                                _sized(v, "bfloat16", "v", at, new), _cache(k_cache, desc, "k_cache", options),
                                 _cache(v_cache, desc, "v_cache", options),
-                                _dev(block_tables, "int32", "block_tables"),
-                                _dev(context_lens, "int32", "context_lens"), n,
-                                int(max_context_len), float(scale), _dev(out, "bfloat16", "out"), ws,
-                                wbytes, ctypes.byref(desc),
+                                _sized(block_tables, "int32", "block_tables", at, tables),
+                                _sized(context_lens, "int32", "context_lens", at, n), n,
+                                int(max_context_len), float(scale), _sized(out, "bfloat16", "out", at, rows),
+                                _scratch(workspace, at), wbytes, ctypes.byref(desc),
                                 ctypes.byref(options) if options is not None else None,
                                 _stream(stream)), "pa_append_decode")
 
@@ -544,11 +579,12 @@ def pa_decode_noalloc(q, k_cache, v_cache, block_tables, context_lens, max_conte
                       stream=None, num_seqs: int | None = None) -> None:
     """pa_decode with the library's fixed scratch array instead of a caller workspace."""
     n = int(context_lens.shape[0]) if num_seqs is None else int(num_seqs)
-    _check(lib.pa_decode_noalloc(_dev(q, "bfloat16", "q"), _cache(k_cache, desc, "k_cache", options),
+    at, rows, _, tables = _decode_sizes(desc, options, n)
+    _check(lib.pa_decode_noalloc(_sized(q, "bfloat16", "q", at, rows), _cache(k_cache, desc, "k_cache", options),
                                  _cache(v_cache, desc, "v_cache", options),
-                                 _dev(block_tables, "int32", "block_tables"),
-                                 _dev(context_lens, "int32", "context_lens"), n,
-                                 int(max_context_len), float(scale), _dev(out, "bfloat16", "out"),
+                                 _sized(block_tables, "int32", "block_tables", at, tables),
+                                 _sized(context_lens, "int32", "context_lens", at, n), n,
+                                 int(max_context_len), float(scale), _sized(out, "bfloat16", "out", at, rows),
                                  ctypes.byref(desc),
                                  ctypes.byref(options) if options is not None else None,
                                  _stream(stream)), "pa_decode_noalloc")
