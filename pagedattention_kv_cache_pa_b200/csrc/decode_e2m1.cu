@@ -581,7 +581,8 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
             for (int jj = 0; jj < 2; ++jj) {
                 const int col = nt * 8 + 2 * c + jj, tok = kRows ? col / G : 0, h = col - tok * G;
                 if (kRows ? tok >= ntok : h >= G) continue;
-                const float inv = l_run[nt][jj] == 0.f ? 0.f : p.out_scale / l_run[nt][jj];
+                // the scale only after the division: a small one over a long context's sum is no float
+                const float inv = l_run[nt][jj] == 0.f ? 0.f : 1.f / l_run[nt][jj], os = p.out_scale;
                 // the lane's D / 8 dims r D / 8 ..: consecutive pairs
                 if (whole) {
                     uint4* out = reinterpret_cast<uint4*>(
@@ -589,16 +590,16 @@ __global__ void __launch_bounds__(kThreads, (ECfg<D, NT>::kMinBlocks))
 #pragma unroll
                     for (int i = 0; i < W; ++i)
                         out[i] = make_uint4(
-                            pack_bf16x2(o_acc[nt][4 * i][jj] * inv, o_acc[nt][4 * i][jj + 2] * inv),
-                            pack_bf16x2(o_acc[nt][4 * i + 1][jj] * inv, o_acc[nt][4 * i + 1][jj + 2] * inv),
-                            pack_bf16x2(o_acc[nt][4 * i + 2][jj] * inv, o_acc[nt][4 * i + 2][jj + 2] * inv),
-                            pack_bf16x2(o_acc[nt][4 * i + 3][jj] * inv, o_acc[nt][4 * i + 3][jj + 2] * inv));
+                            pack_bf16x2(o_acc[nt][4 * i][jj] * inv * os, o_acc[nt][4 * i][jj + 2] * inv * os),
+                            pack_bf16x2(o_acc[nt][4 * i + 1][jj] * inv * os, o_acc[nt][4 * i + 1][jj + 2] * inv * os),
+                            pack_bf16x2(o_acc[nt][4 * i + 2][jj] * inv * os, o_acc[nt][4 * i + 2][jj + 2] * inv * os),
+                            pack_bf16x2(o_acc[nt][4 * i + 3][jj] * inv * os, o_acc[nt][4 * i + 3][jj + 2] * inv * os));
                 } else {
                     float4* po = reinterpret_cast<float4*>(p.part_o + (prow + col) * D + r * (D / 8));
 #pragma unroll
                     for (int i = 0; i < 2 * W; ++i)
-                        po[i] = make_float4(o_acc[nt][2 * i][jj] * inv, o_acc[nt][2 * i][jj + 2] * inv,
-                                            o_acc[nt][2 * i + 1][jj] * inv, o_acc[nt][2 * i + 1][jj + 2] * inv);
+                        po[i] = make_float4(o_acc[nt][2 * i][jj] * inv * os, o_acc[nt][2 * i][jj + 2] * inv * os,
+                                            o_acc[nt][2 * i + 1][jj] * inv * os, o_acc[nt][2 * i + 1][jj + 2] * inv * os);
                     if (r == 0)
                         p.part_lse[prow + col] = l_run[nt][jj] == 0.f ? -FLT_MAX : m_run[nt][jj] + __log2f(l_run[nt][jj]);
                 }

@@ -134,6 +134,11 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 // P in V's type
 template <bool kE2m1>
 __device__ __forceinline__ uint32_t pack_p(float lo, float hi) {
@@ -844,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_after_sync();
             const int tok = R / G, gq = R - tok * G;
-            const float inv = kSplit && l_run == 0.f ? 0.f : p.out_scale / l_run;
+            const float inv = kSplit && l_run == 0.f ? 0.f : 1.f / l_run;
             const size_t part = part_row(it);
             if (kSplit && it.piece) p.part_lse[part] = l_run == 0.f ? -FLT_MAX : m_run + __log2f(l_run);
             uint16_t* out = p.out + ((size_t)(it.q0 + tok) * Hq + (size_t)it.kvh * G + gq) * D;
@@ -852,20 +857,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int h = 0; h < D / 32; ++h) {
                 uint32_t o[32];
                 tmem_ld32(t_o + h * 32, o);                  // warp-wide: padded rows join the load
+                // V's scale only after the division: a small one over a long context's sum is no float.  (By
+                // pairs: one by one, the 1021 rows of 15000 took 640 us for 630.)
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                    uint64_t y = f2_mul(f2(__uint_as_float(o[j]), __uint_as_float(o[j + 1])), f2(inv, inv));
+                    if (kE2m1) y = f2_mul(y, f2(p.out_scale, p.out_scale));
+                    float lo, hi;
+                    f2_split(y, lo, hi);
+                    o[j] = __float_as_uint(lo), o[j + 1] = __float_as_uint(hi);
+                }
                 if (kSplit && it.piece) {
                     float4* po = part_dims<D>(p.part_o, part) + h * 8 * kRows;   // a warp's rows side by side
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
-                        po[c * kRows] = make_float4(__uint_as_float(o[4 * c]) * inv, __uint_as_float(o[4 * c + 1]) * inv,
-                                            __uint_as_float(o[4 * c + 2]) * inv, __uint_as_float(o[4 * c + 3]) * inv);
+                        po[c * kRows] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
+                                                    __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
                 } else if (R < it.rows) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint4 w;
-                        w.x = pack_bf16x2(__uint_as_float(o[8 * c + 0]) * inv, __uint_as_float(o[8 * c + 1]) * inv);
-                        w.y = pack_bf16x2(__uint_as_float(o[8 * c + 2]) * inv, __uint_as_float(o[8 * c + 3]) * inv);
-                        w.z = pack_bf16x2(__uint_as_float(o[8 * c + 4]) * inv, __uint_as_float(o[8 * c + 5]) * inv);
-                        w.w = pack_bf16x2(__uint_as_float(o[8 * c + 6]) * inv, __uint_as_float(o[8 * c + 7]) * inv);
+                        w.x = pack_bf16x2(__uint_as_float(o[8 * c + 0]), __uint_as_float(o[8 * c + 1]));
+                        w.y = pack_bf16x2(__uint_as_float(o[8 * c + 2]), __uint_as_float(o[8 * c + 3]));
+                        w.z = pack_bf16x2(__uint_as_float(o[8 * c + 4]), __uint_as_float(o[8 * c + 5]));
+                        w.w = pack_bf16x2(__uint_as_float(o[8 * c + 6]), __uint_as_float(o[8 * c + 7]));
                         *reinterpret_cast<uint4*>(out + h * 32 + 8 * c) = w;
                     }
                 }
