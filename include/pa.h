@@ -276,7 +276,8 @@ PA_API size_t pa_decode_workspace_size_ex(int32_t num_seqs, int32_t max_context_
  * row is turned and rounded to bf16 first, and that bf16 row is quantized.
  *
  * options->kv_dtype == PA_KV_E2M1: the caches are 4-bit pools (see
- * pa_append_kv_e2m1), for any number of kv heads; kernel PA_KERNEL_AUTO or
+ * pa_append_kv_e2m1), for any number of kv heads; scale * k_scale * log2(e) has to be
+ * a finite float (PA_ERR_INVALID); kernel PA_KERNEL_AUTO or
  * PA_KERNEL_TENSOR (PA_ERR_UNSUPPORTED otherwise).  q is used as f16 after a
  * power of two per row, P as f16 after another: a weight is rounded by 2^-12 of
  * itself down to 2^-25 of the largest score's, and by 2^-36 of that one's below.
@@ -371,7 +372,7 @@ PA_API int pa_prefill(const pa_bf16* q, const pa_bf16* k_cache, const pa_bf16* v
 /*
  * pa_prefill over a cache of any built type.  options (NULL: all zero): kernel as for
  * pa_prefill; kv_dtype PA_KV_BF16 or PA_KV_E2M1 (4-bit pools, see pa_append_kv_e2m1, with
- * their scales; block sizes of 4-bit pools; kernel PA_PREFILL_TCGEN05_WS: tiles of 256 query
+ * their scales, scale * k_scale * log2(e) a finite float; block sizes of 4-bit pools; kernel PA_PREFILL_TCGEN05_WS: tiles of 256 query
  * rows; PA_PREFILL_ROWS: the decode kernel with several rows' heads for its columns, Hq / Hkv <= 16;
  * PA_PREFILL_AUTO: the latter for few rows).
  * 4-bit K is widened to bf16 (rows: f16, as q is after a power of two per row) and V to f16

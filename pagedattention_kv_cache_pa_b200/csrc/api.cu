@@ -50,6 +50,9 @@ int check_e2m1_desc(const pa_cache_desc* d) {
 // A scale of a quantized cache tensor: it and its reciprocal positive and finite.
 bool good_scale(float s) { return s > 0.f && s < INFINITY && 1.f / s < INFINITY; }
 
+// What multiplies a score over K of this scale (in the log2 domain) is a finite float.
+bool good_score_scale(float scale, float k_scale) { return fabsf(scale * k_scale * 1.4426950408889634f) < INFINITY; }
+
 // Optional override of the automatic split size, for tuning sweeps.
 int32_t env_split_tokens() {
     static int32_t v = [] {
@@ -485,7 +488,9 @@ static int decode_call(const pa_bf16* q, const pa_bf16* k_new, const pa_bf16* v_
     const float rope_theta = options ? options->rope_theta : 0.f;
     const bool e2m1 = options && options->kv_dtype == PA_KV_E2M1;
     const bool fp8 = options && options->kv_dtype == PA_KV_E4M3, scaled = fp8 || e2m1;
-    if (e2m1 && (!good_scale(options->k_scale) || !good_scale(options->v_scale))) return PA_ERR_INVALID;
+    if (e2m1 && (!good_scale(options->k_scale) || !good_scale(options->v_scale) ||
+                 !good_score_scale(scale, options->k_scale)))
+        return PA_ERR_INVALID;
     if (fp8 && (!(options->k_scale > 0.f) || !(options->k_scale < INFINITY) ||
                 !(options->v_scale > 0.f) || !(options->v_scale < INFINITY)))
         return PA_ERR_INVALID;
@@ -752,7 +757,8 @@ extern "C" int pa_prefill_ex(const void* q, const void* k_cache, const void* v_c
                           options ? options->kernel : PA_PREFILL_AUTO, stream);
     rc = check_desc(desc);
     if (rc != PA_OK) return rc;
-    if (num_seqs < 0 || num_seqs > 65535 || max_q_len < 0 || !(scale > 0.f) || !(scale < INFINITY))
+    if (num_seqs < 0 || num_seqs > 65535 || max_q_len < 0 || !(scale > 0.f) || !(scale < INFINITY) ||
+        !good_score_scale(scale, options->k_scale))
         return PA_ERR_INVALID;
     rc = check_e2m1_desc(desc);
     if (rc != PA_OK) return rc;
