@@ -42,6 +42,8 @@
  *                     are never read
  *   context_lens      [num_seqs] int32: tokens the decode query attends to,
  *                     the token appended this step included
+ *                     (at most 2^31 - 256: a longer sequence counts as one past
+ *                     its table)
  * Query head h reads kv head h / (num_q_heads / num_kv_heads).
  */
 #ifndef PA_H_

@@ -287,6 +287,7 @@ static PrefillParams prefill_params(const void* q, const void* k_cache, const vo
     p.head_dim = d.head_dim;
     p.group = d.num_q_heads / d.num_kv_heads;
     p.max_blocks_per_seq = d.max_blocks_per_seq;
+    p.len_cap = longest_sequence(d, INT32_MAX);
     p.max_q_len = max_q_len;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.out_scale = 1.f;
@@ -540,6 +541,7 @@ static int decode_call(const pa_bf16* q, const pa_bf16* k_new, const pa_bf16* v_
     p.group = desc->num_q_heads / desc->num_kv_heads;
     p.max_blocks_per_seq = desc->max_blocks_per_seq;
     p.max_context_len = max_context_len;
+    p.len_cap = longest_sequence(*desc, max_context_len);
     p.split_tokens = plan.split_tokens;
     p.max_splits = plan.max_splits;
     p.scale_log2 = scale * (scaled ? options->k_scale : 1.f) * 1.4426950408889634f;
@@ -803,6 +805,7 @@ extern "C" int pa_prefill_ex(const void* q, const void* k_cache, const void* v_c
         dp.group = desc->num_q_heads / desc->num_kv_heads;
         dp.max_blocks_per_seq = desc->max_blocks_per_seq;
         dp.max_context_len = max_context_len;
+        dp.len_cap = longest_sequence(*desc, max_context_len);
         dp.scale_log2 = scale * options->k_scale * 1.4426950408889634f;
         dp.out_scale = options->v_scale;
         dp.grid = r.slices;

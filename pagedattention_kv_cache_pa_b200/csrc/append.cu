@@ -53,8 +53,7 @@ __global__ void __launch_bounds__(256) append_at_end_kernel(const DecodeParams p
         const int32_t b = (int32_t)(i / per_seq);
         const int64_t within = i - (int64_t)b * per_seq;
         const int32_t L = p.context_lens[b];
-        const int32_t cap = p.max_blocks_per_seq * p.block_size;
-        if (L <= 0 || L > cap || L > p.max_context_len) continue;
+        if (L <= 0 || L > p.len_cap) continue;
         const int32_t pos = L - 1;
         const int32_t blk = p.block_tables[(size_t)b * p.max_blocks_per_seq + pos / p.block_size];
         if (blk < 0 || blk >= p.num_blocks) continue;

@@ -50,11 +50,9 @@ __device__ __forceinline__ void raise_status(int32_t* status, int32_t bit) {
 // A context length as the decode uses it: negative or past what the table (and the call's
 // max_context_len) can hold is reported and clipped.
 __device__ __forceinline__ int32_t clip_length(const DecodeParams& p, int32_t L) {
-    const int32_t table_cap = p.max_blocks_per_seq * p.block_size;
-    const int32_t cap = p.max_context_len < table_cap ? p.max_context_len : table_cap;
-    if (L < 0 || L > cap) {
+    if (L < 0 || L > p.len_cap) {
         raise_status(p.status, kStatusBadLength);
-        L = L < 0 ? 0 : cap;
+        L = L < 0 ? 0 : p.len_cap;
     }
     return L;
 }
@@ -73,7 +71,7 @@ __device__ __forceinline__ int32_t rows_length(const DecodeParams& p, int32_t v,
     row0 = q0 + first;
     n = min(p.q_tokens, Tq - first);
     if (n <= 0) return 0;
-    if (L < Tq || (int64_t)L > (int64_t)p.max_blocks_per_seq * p.block_size || L > p.max_context_len || Tq > p.max_q_len) {
+    if (L < Tq || L > p.len_cap || Tq > p.max_q_len) {
         raise_status(p.status, kStatusBadLength);
         return 0;
     }

@@ -42,6 +42,7 @@ struct DecodeParams {
     int32_t group;                 // Hq / Hkv
     int32_t max_blocks_per_seq;
     int32_t max_context_len;
+    int32_t len_cap;               // longest sequence of the call: max_context_len, as far as the table holds it
     int32_t split_tokens;          // C: tokens per split (multiple of 64)
     int32_t max_splits;            // S = ceil(max_context_len / C)
     float scale_log2;              // scale * log2(e): scores are kept in the log2 domain
@@ -93,6 +94,7 @@ struct PrefillParams {
     int32_t* status;
     int32_t num_seqs, num_blocks, block_size, num_kv_heads, num_q_heads, head_dim, group;
     int32_t max_blocks_per_seq;
+    int32_t len_cap;               // longest sequence that the table holds
     int32_t max_q_len;             // the caller's bound on every sequence's query count
     float scale_log2;
     float out_scale;               // multiplies the normalised output (4-bit pools: the V scale)
@@ -123,6 +125,14 @@ constexpr size_t kWorkspaceAlign = 256;
 // (whose stalled waits are meant to run out quickly).
 constexpr unsigned long long kDecodeWaitNs = 2000000000ull;   // 2 s
 constexpr unsigned long long kSelftestWaitNs = 10000000ull;   // 10 ms
+
+// Tokens of a sequence at most: what its table row holds, formed in 64 bits, and few enough that a position
+// past the end, up to the end of a kernel's tile, is a 32-bit number.
+inline int32_t longest_sequence(const pa_cache_desc& d, int32_t bound) {
+    int64_t n = (int64_t)d.max_blocks_per_seq * d.block_size;
+    n = n < INT32_MAX - 255 ? n : INT32_MAX - 255;
+    return (int32_t)(bound < n ? bound : n);
+}
 
 int num_sms_current_device(int* out);
 int make_decode_plan(int32_t num_seqs, int32_t max_context_len, const pa_cache_desc& d,

@@ -176,7 +176,7 @@ __device__ __forceinline__ int ws_item(const PrefillParams& p, long long i, WsIt
     it.Tq = p.cu_q[it.b + 1] - it.q0;
     it.L = p.context_lens[it.b];
     if (it.Tq <= 0) return 0;
-    if ((kCausal ? it.L < it.Tq : it.L < 0) || it.L > p.max_blocks_per_seq * p.block_size || it.Tq > p.max_q_len)
+    if ((kCausal ? it.L < it.Tq : it.L < 0) || it.L > p.len_cap || it.Tq > p.max_q_len)
         return -1;
     it.rows = it.Tq * p.group;
     const int tile = (it.rows + kWsRows - 1) / kWsRows - 1 - t_rev;
@@ -211,7 +211,7 @@ __device__ __forceinline__ CrossSeq cross_seq(const PrefillParams& p, int b) {
     c.q0 = p.cu_q[b];
     c.Tq = p.cu_q[b + 1] - c.q0;
     c.L = p.context_lens[b];
-    c.bad = c.Tq > 0 && (c.L < 0 || c.L > (long long)p.max_blocks_per_seq * p.block_size || c.Tq > p.max_q_len);
+    c.bad = c.Tq > 0 && (c.L < 0 || c.L > p.len_cap || c.Tq > p.max_q_len);
     c.row_tiles = c.Tq <= 0 || c.bad ? 0 : (c.Tq * p.group + kWsRows - 1) / kWsRows;
     c.nt = c.L > 0 ? (c.L - 1) / kWsKeys + 1 : 1;
     c.tiles = (long long)c.row_tiles * p.num_kv_heads * c.nt;
