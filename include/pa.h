@@ -285,7 +285,8 @@ PA_API size_t pa_decode_workspace_size_ex(int32_t num_seqs, int32_t max_context_
  * itself down to 2^-25 of the largest score's, and by 2^-36 of that one's below.
  * pa_append_decode quantizes the new rows as
  * pa_append_kv_e2m1 (pa_rope_append_kv_e2m1 with rope_theta > 0) does, in a
- * launch of its own before the decode.
+ * launch of its own before the decode; a sequence whose length is clipped keeps
+ * its rows as they are.
  *
  * PA_FLAG_PDL (whole-group and 4-bit tensor kernels; ignored by the others): the
  * decode kernel is launched as a programmatic dependent of the kernel before

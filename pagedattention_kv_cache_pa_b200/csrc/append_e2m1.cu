@@ -113,11 +113,11 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
             const int32_t t = (int32_t)(t0 + tl);
             int32_t pos;
             if (kAtEnd) {
-                const int32_t L = clipped_length(p, t);
+                const int32_t given = p.context_lens[t], L = clip_length(p, given);
                 pos = L > 0 ? L - 1 : 0;
                 if (j == 0) {
                     int64_t slot = -1;
-                    if (L > 0) {
+                    if (L > 0 && L == given) {               // where a clipped length ends another token stands
                         const int32_t blk = p.block_tables[(size_t)t * p.max_blocks_per_seq + pos / a.Bs];
                         if (blk >= 0 && blk < p.num_blocks) slot = (int64_t)blk * a.Bs + pos % a.Bs;
                     }
