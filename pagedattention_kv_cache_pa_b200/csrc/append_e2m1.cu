@@ -88,9 +88,9 @@ __global__ void __launch_bounds__(kThreads) append_e2m1_kernel(const E2m1Args a,
 // with their first loads of q already under way; from then on a ninth warp forms the next tile's
 // while the others work on this one.  (Formed between two barriers by all, they were a third of the
 // time.)  Bound by the loads' latency and DRAM: 16384 tokens of 64 + 2 x 8 heads of 128 take, with their
-// read-back, 141 us (690 MB, 76 % of the copy rate) with three CTAs an SM of two rows in flight a thread, 144
-// with two CTAs of four, 154 with three of four or four of two (spills), 168 with the next tile's rows
-// requested into L2 ahead.
+// read-back, 141 us (690 MB, 76 % of the copy rate) with three CTAs an SM of two rows in flight a thread (which
+// spill 20 bytes a thread), 144 with two CTAs of four, 154 with three of four or four of two (which spill more),
+// 168 with the next tile's rows requested into L2 ahead.
 constexpr int kMaxTokens = 8;
 constexpr int kRopeThreads = kThreads + 32, kRopeCtas = 3;   // CTAs an SM
 
@@ -286,14 +286,13 @@ int tokens_per_cta(int32_t T, int most, int ctas) {
     const int spread = (T + ctas - 1) / ctas;
     return spread < most ? (spread < 1 ? 1 : spread) : most;
 }
-unsigned rope_grid(int32_t T, int tpc) {   // resident at once: a CTA's later tiles have their angles ready
+// CTAs for tiles of tpc tokens, at most `most`.  The rotating kernel's are all resident at once: a CTA's later
+// tiles have their angles ready.
+unsigned grid_for(int32_t T, int tpc, int most) {
     const int64_t g = ((int64_t)T + tpc - 1) / tpc;
-    return (unsigned)(g < 148 * kRopeCtas ? g : 148 * kRopeCtas);
+    return (unsigned)(g < most ? g : most);
 }
-unsigned grid_for(int32_t T, int tpc) {
-    const int64_t g = ((int64_t)T + tpc - 1) / tpc;
-    return (unsigned)(g < 148 * 8 ? g : 148 * 8);
-}
+constexpr int kPlainCtas = 8, kPlainSpread = 2;   // CTAs an SM at most without rotation; those a small call spreads over
 
 }  // namespace
 
@@ -302,28 +301,32 @@ cudaError_t launch_append_e2m1(const pa_bf16* q, pa_bf16* q_out, const pa_bf16* 
                                float v_inv, uint8_t* k_cache, uint8_t* v_cache, const pa_cache_desc& d,
                                cudaStream_t stream) {
     if (T == 0) return cudaSuccess;
+    int sms = 0;
+    if (num_sms_current_device(&sms) != PA_OK) return cudaErrorInvalidDevice;
     E2m1Args a{q, q_out, k, v, positions, slots, T, d.num_q_heads, d.num_kv_heads, d.block_size,
                (int64_t)d.num_blocks * d.block_size, theta, k_inv, v_inv, k_cache, v_cache};
     const int D = d.head_dim;
     if (theta > 0.f) {
-        const int tpc = tokens_per_cta(T, kMaxTokens, 148 * kRopeCtas);
+        const int tpc = tokens_per_cta(T, kMaxTokens, sms * kRopeCtas);
         const DecodeParams none{};
         if (D == 64)
-            rope_append_e2m1_kernel<64, false><<<rope_grid(T, tpc), kRopeThreads, 0, stream>>>(a, none, tpc);
+            rope_append_e2m1_kernel<64, false><<<grid_for(T, tpc, sms * kRopeCtas), kRopeThreads, 0, stream>>>(a, none, tpc);
         else
-            rope_append_e2m1_kernel<128, false><<<rope_grid(T, tpc), kRopeThreads, 0, stream>>>(a, none, tpc);
+            rope_append_e2m1_kernel<128, false><<<grid_for(T, tpc, sms * kRopeCtas), kRopeThreads, 0, stream>>>(a, none, tpc);
     } else {
-        const int tpc = tokens_per_cta(T, 8, 296);
+        const int tpc = tokens_per_cta(T, 8, sms * kPlainSpread);
         if (D == 64)
-            append_e2m1_kernel<64><<<grid_for(T, tpc), kThreads, 0, stream>>>(a, tpc);
+            append_e2m1_kernel<64><<<grid_for(T, tpc, sms * kPlainCtas), kThreads, 0, stream>>>(a, tpc);
         else
-            append_e2m1_kernel<128><<<grid_for(T, tpc), kThreads, 0, stream>>>(a, tpc);
+            append_e2m1_kernel<128><<<grid_for(T, tpc, sms * kPlainCtas), kThreads, 0, stream>>>(a, tpc);
     }
     return cudaGetLastError();
 }
 
 cudaError_t launch_append_e2m1_at_end(const DecodeParams& p, uint16_t* q_out, cudaStream_t stream) {
     if (p.num_seqs == 0) return cudaSuccess;
+    int sms = 0;
+    if (num_sms_current_device(&sms) != PA_OK) return cudaErrorInvalidDevice;
     E2m1Args a{p.q, p.rope_theta > 0.f ? q_out : nullptr, p.k_new, p.v_new, nullptr, nullptr, p.num_seqs,
                p.num_q_heads, p.num_kv_heads, p.block_size, (int64_t)p.num_blocks * p.block_size, p.rope_theta,
                p.k_inv_scale, p.v_inv_scale,
@@ -331,11 +334,11 @@ cudaError_t launch_append_e2m1_at_end(const DecodeParams& p, uint16_t* q_out, cu
                reinterpret_cast<uint8_t*>(const_cast<uint16_t*>(p.k_cache)),
                reinterpret_cast<uint8_t*>(const_cast<uint16_t*>(p.v_cache))};
     const int D = p.head_dim;
-    const int tpc = tokens_per_cta(p.num_seqs, kMaxTokens, 148 * kRopeCtas);
+    const int tpc = tokens_per_cta(p.num_seqs, kMaxTokens, sms * kRopeCtas);
     if (D == 64)
-        rope_append_e2m1_kernel<64, true><<<rope_grid(p.num_seqs, tpc), kRopeThreads, 0, stream>>>(a, p, tpc);
+        rope_append_e2m1_kernel<64, true><<<grid_for(p.num_seqs, tpc, sms * kRopeCtas), kRopeThreads, 0, stream>>>(a, p, tpc);
     else
-        rope_append_e2m1_kernel<128, true><<<rope_grid(p.num_seqs, tpc), kRopeThreads, 0, stream>>>(a, p, tpc);
+        rope_append_e2m1_kernel<128, true><<<grid_for(p.num_seqs, tpc, sms * kRopeCtas), kRopeThreads, 0, stream>>>(a, p, tpc);
     return cudaGetLastError();
 }
 
@@ -343,14 +346,16 @@ cudaError_t launch_gather_e2m1(const uint8_t* k_cache, const uint8_t* v_cache, c
                                float k_scale, float v_scale, pa_bf16* k, pa_bf16* v, const pa_cache_desc& d,
                                cudaStream_t stream) {
     if (T == 0) return cudaSuccess;
+    int sms = 0;
+    if (num_sms_current_device(&sms) != PA_OK) return cudaErrorInvalidDevice;
     E2m1Args a{nullptr, nullptr, nullptr, nullptr, nullptr, slots, T, d.num_q_heads, d.num_kv_heads, d.block_size,
                (int64_t)d.num_blocks * d.block_size, 0.f, k_scale, v_scale, const_cast<uint8_t*>(k_cache),
                const_cast<uint8_t*>(v_cache)};
-    const int tpc = tokens_per_cta(T, 8, 296);
+    const int tpc = tokens_per_cta(T, 8, sms * kPlainSpread);
     if (d.head_dim == 64)
-        gather_e2m1_kernel<64><<<grid_for(T, tpc), kThreads, 0, stream>>>(a, k, v, tpc);
+        gather_e2m1_kernel<64><<<grid_for(T, tpc, sms * kPlainCtas), kThreads, 0, stream>>>(a, k, v, tpc);
     else
-        gather_e2m1_kernel<128><<<grid_for(T, tpc), kThreads, 0, stream>>>(a, k, v, tpc);
+        gather_e2m1_kernel<128><<<grid_for(T, tpc, sms * kPlainCtas), kThreads, 0, stream>>>(a, k, v, tpc);
     return cudaGetLastError();
 }
 
