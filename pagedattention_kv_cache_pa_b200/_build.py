@@ -2,6 +2,7 @@
 from __future__ import annotations
 
 import os
+import re
 import subprocess
 import sys
 
@@ -19,6 +20,19 @@ HEADERS = ["pa_internal.h", "pa_device.cuh", "pa_ptx.cuh", "pa_umma.cuh", "pa_e2
 NVCC_FLAGS = ["-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
               "--expt-relaxed-constexpr", "-Xptxas", "-v"]
+
+# Kernels that move registers between their warps (setmaxnreg), whose shares add up to this launch number: the
+# launch refuses another, so a build that came out with one is no build.
+LAUNCH_REGISTERS = {"prefill_wide.cu": ("prefill_wide_kernel", 128)}
+
+
+def check_registers(ptxas: str, kernel: str, want: int) -> int:
+    """Number of `kernel`'s instantiations in ptxas' report; raises if one has not `want` registers."""
+    entries = re.findall(r"Compiling entry function '(\w+)'.*?Used (\d+) registers", ptxas, re.S)
+    got = [int(n) for name, n in entries if kernel in name]
+    if not got or any(n != want for n in got):
+        raise RuntimeError("%s: %s registers a thread, its warps' shares are for %d" % (kernel, got or "no", want))
+    return len(got)
 
 
 def _nvcc() -> str:
@@ -47,6 +61,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
             if res.returncode != 0:
                 sys.stderr.write(res.stdout + res.stderr)
                 raise RuntimeError("nvcc failed on %s" % src)
+            if src in LAUNCH_REGISTERS:
+                try:
+                    check_registers(res.stderr, *LAUNCH_REGISTERS[src])
+                except RuntimeError:
+                    os.remove(o)               # the next build compiles it again
+                    raise
             with open(o + ".ptxas.txt", "w") as f:
                 f.write(res.stderr)
             if verbose:
