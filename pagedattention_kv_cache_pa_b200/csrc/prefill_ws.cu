@@ -881,7 +881,8 @@ int cross_ws_slices(int32_t num_seqs, int32_t num_kv_heads, int32_t group, int32
 }
 
 cudaError_t launch_cross_ws(const PrefillParams& p, int max_q_len, cudaStream_t stream) {
-    if (p.head_dim == 128) return launch_ws<128, false, true>(p, max_q_len, stream);   // others: prefill_wide.cu
+    if (p.head_dim == 128)                                   // whole items: prefill_wide.cu
+        return p.cuts ? launch_ws<128, false, true>(p, max_q_len, stream) : cudaErrorInvalidValue;
     return p.cuts ? launch_ws<64, false, true>(p, max_q_len, stream) : launch_ws<64, false, false>(p, max_q_len, stream);
 }
 
