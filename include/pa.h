@@ -170,8 +170,8 @@ PA_API int pa_rope_append_kv(const pa_bf16* q, pa_bf16* q_out, const pa_bf16* k,
 PA_API size_t pa_kv_cache_bytes(const pa_cache_desc* desc, int32_t kv_dtype);
 
 /* pa_append_kv into 4-bit pools: the same slots and rules (a skipped token's bytes, and every
- * other token's, stay as they are); k_scale, v_scale: gs of each cache, positive and finite as
- * are their reciprocals. */
+ * other token's, stay as they are; of two tokens in one slot, codes and scales may come from
+ * either); k_scale, v_scale: gs of each cache, positive and finite as are their reciprocals. */
 PA_API int pa_append_kv_e2m1(const pa_bf16* k, const pa_bf16* v, const int64_t* slot_mapping,
                              int32_t num_tokens, float k_scale, float v_scale, uint8_t* k_cache,
                              uint8_t* v_cache, const pa_cache_desc* desc, void* stream);
@@ -347,9 +347,10 @@ PA_API int pa_append_decode(const pa_bf16* q, const pa_bf16* k, const pa_bf16* v
  * K_j, V_j of kv head h / (Hq/Hkv).  fp32 accumulation, online softmax.
  * cu_seqlens_q: [num_seqs + 1] int32 device array (0 first, non-decreasing);
  * max_q_len >= every Tq (sizes the grid).  workspace: >= 256 bytes, 256-byte
- * aligned, its status word as for pa_decode (a block id outside the pool, or
- * L < Tq, L past the table or Tq > max_q_len: the sequence's rows are left
- * unwritten and pa_decode_status reports it).  head_dim 64 or 128.
+ * aligned, its status word as for pa_decode (L < Tq, L past the table or
+ * Tq > max_q_len: the sequence's rows are left unwritten; a block id outside the
+ * pool: the values of that sequence's rows are unspecified; pa_decode_status
+ * reports either).  head_dim 64 or 128.
  * kernel: PA_PREFILL_AUTO (PA_PREFILL_TCGEN05_WS where it serves the block
  * size, else PA_PREFILL_TCGEN05), PA_PREFILL_TCGEN05 (128-row tiles on the
  * fifth-generation tensor cores, accumulators in tensor memory),
@@ -373,7 +374,7 @@ PA_API int pa_prefill(const pa_bf16* q, const pa_bf16* k_cache, const pa_bf16* v
                       const pa_cache_desc* desc, int32_t kernel, void* stream);
 
 /*
- * pa_prefill over a cache of any built type.  options (NULL: all zero): kernel as for
+ * pa_prefill over a bf16 or a 4-bit cache.  options (NULL: all zero): kernel as for
  * pa_prefill; kv_dtype PA_KV_BF16 or PA_KV_E2M1 (4-bit pools, see pa_append_kv_e2m1, with
  * their scales, scale * k_scale * log2(e) a finite float; block sizes of 4-bit pools; kernel PA_PREFILL_TCGEN05_WS: tiles of 256 query
  * rows; PA_PREFILL_ROWS: the decode kernel with several rows' heads for its columns, Hq / Hkv <= 16;
@@ -420,7 +421,9 @@ PA_API int pa_prefill_ex(const void* q, const void* k_cache, const void* v_cache
  * arguments, else: of these or larger ones), 256-byte aligned,
  * zero-filled before its first use, one per call in flight; its status word as for pa_decode
  * (more rows than max_q_len, or a length below zero or past the table: that sequence's rows are
- * left unwritten, or for the NULL form the length clipped, and pa_decode_status reports it).
+ * left unwritten, or for the NULL form the length clipped; a block id outside the pool: the
+ * values of that sequence's rows are unspecified; pa_decode_status reports either).
+ * P is rounded to bf16 (2^-9 of a weight), as in pa_prefill and pa_decode's tensor-core kernels.
  * head_dim 64 or 128; block sizes 8, 16, 32, 64 or multiples of 64.
  * Errors: PA_ERR_INVALID, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE, PA_ERR_CUDA.
  */

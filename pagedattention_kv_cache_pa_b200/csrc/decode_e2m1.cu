@@ -31,7 +31,7 @@
 //
 // Measured (a call inside a CUDA graph, merge included): 32 and 8 heads of 64, 64 sequences up to 2048 tokens
 // 22.5 us, 32 sequences on pages of 256 33 us (2.7 TB/s of 4-bit rows), one of 777 tokens 8.8 us; 64 and 8 heads
-// of 128, 4 sequences up to 131072 88 us (4.1 TB/s).  Bound by instruction issue (64 % of the slots on the
+// of 128, 4 sequences up to 131072 87 us (4.1 TB/s).  Bound by instruction issue (63 % of the slots on the
 // last, 368 warp instructions per 16 keys), and by about 8 us of start, plan and merge.
 #include <cuda_runtime.h>
 #include <float.h>

@@ -32,15 +32,16 @@
 //                   order of two MMAs is given for one accumulator and shape, and these have two.
 //                   While one row tile's products run, the other's softmax has the exponential
 //                   unit to itself; so that it is so from an item's start, the second row tile's
-//                   first scores follow the first's second (153 -> 147 us and 630 -> 613 below).
+//                   first scores follow the first's second (153 -> 147 us with 64 dims below).
 // K and V tiles have rings of their own.
 //
 // Long prefills of few items: the items of the last, unfilled round are cut (Walk, wide_split_ctas).
 //
-// Measured (a call inside a CUDA graph): 4-bit, 32 and 8 heads of 64, 4 x 2048 rows 147 us (467 TFLOP/s); 64 and
-// 8 heads of 128, the last 1021 rows of 15000 613 us (847 TFLOP/s, the exponentials alone 226 us); cross
-// attention, 32 and 8 heads of 128, 4 x 1024 rows over 4096 tokens 274 us (1000 TFLOP/s).  Bound by a row tile's
-// chain of scores, softmax and products: without the softmax's arithmetic an earlier form of the first two took
+// Measured (a call inside a CUDA graph): 4-bit, 32 and 8 heads of 64, 4 x 2048 rows 149 us (463 TFLOP/s); 64 and
+// 8 heads of 128, the last 1021 rows of 15000 623 us (833 TFLOP/s, the exponentials alone 226 us); cross
+// attention, 32 and 8 heads of 128, 4 x 1024 rows over 4096 tokens 298 us (922 TFLOP/s).  Bound by a row tile's
+// chain of scores, softmax and products (with 128 dims the wait before the next scores too: without it, on the
+// order of issue alone, 613 and 274 us): without the softmax's arithmetic an earlier form of the first two took
 // 125 and 513 us.
 //
 // Every wait is bounded (2 s, then the timeout status bit); the tensor memory is freed and no
@@ -1026,9 +1027,9 @@ cudaError_t launch_wide(const PrefillParams& p, int max_q_len, cudaStream_t stre
 // Whether the last round's items of a 4-bit prefill are cut, as far as the call's bounds tell: the tiles that
 // it would take whole, less those of an even share, against the pieces' way through memory and the merge.
 // Measured (us, cut | whole; tiles saved), the last rows of contexts of the given length: 32 and 8 heads of 64,
-// 300 of 20000 tokens 113 | 316 (115), 512 of 3000 54 | 60 (14), 4 x 256 of 4000 95 | 73 (4), 4000 of 4000
-// 156 | 126 (2); 64 and 8 heads of 128, where the cut's registers are taken from the softmax's, 300 of 20000
-// 262 | 368 (72), 1021 of 15000 610 | 616 (32), 4 x 256 of 4000 212 | 182 (9).
+// 300 of 20000 tokens 111 | 300 (115), 512 of 3000 48 | 53 (14), 4 x 256 of 4000 92 | 68 (4), 4000 of 4000
+// 155 | 125 (2); 64 and 8 heads of 128, where the cut's registers are taken from the softmax's, 300 of 20000
+// 286 | 373 (72), 1021 of 15000 575 | 585 (32), 4 x 256 of 4000 202 | 175 (9).
 int wide_split_ctas(int32_t num_seqs, int32_t num_kv_heads, int32_t group, int32_t head_dim, int32_t max_q_len,
                     int64_t max_len) {
     int sms = 0;
@@ -1055,8 +1056,8 @@ cudaError_t launch_prefill_e2m1(const PrefillParams& p, int max_q_len, cudaStrea
 
 // Cross attention.  With 128 dims these tiles; with 64 dims those of prefill_ws.cu, two CTAs an SM of
 // 128 rows each.  Measured (us, these | prefill_ws.cu), 16 heads: 8 x 448 rows over 1500 tokens, 128
-// dims 67 | 122, 64 dims 59 | 55; 32 x 100 over 500, 128 dims 49 | 52, 64 dims 42 | 25; 32 and 8 heads,
-// 4 x 1024 over 4096, 128 dims 274 (1000 TFLOP/s) | 505, 64 dims 264 | 241.  A call of few items
+// dims 71 | 122, 64 dims 59 | 55; 32 x 100 over 500, 128 dims 50 | 52, 64 dims 42 | 25; 32 and 8 heads,
+// 4 x 1024 over 4096, 128 dims 298 (922 TFLOP/s) | 505, 64 dims 264 | 241.  A call of few items
 // (p.cuts) goes to the stream of key tiles there.
 cudaError_t launch_cross(const PrefillParams& p, int max_q_len, cudaStream_t stream) {
     if (p.head_dim == 128 && !p.cuts) return launch_wide<128, false, false, false>(p, max_q_len, stream);

@@ -867,8 +867,8 @@ int cross_ws_resident(int head_dim) {
 // idle ones take, and costs the states' way through memory and the merge: about 16 tiles' time with 64 dims,
 // 12 with 128.  Measured (us, stream | whole items), 16 heads: 64 dims, 1 x 4 rows over 1500 tokens 15.2 | 25.0,
 // 1 x 448 23.2 | 25.9, 4 x 200 28.7 | 26.5, 8 x 448 61.4 | 55.7; 128 dims (whole items: prefill_wide.cu), 1 x 4
-// 17.6 | 28.7, 1 x 448 31.4 | 33.5, 4 x 200 44.2 | 33.9.  8 heads: 1 x 64 over 8000, 64 dims 24.7 | 107, 128 dims
-// 28.2 | 122; 1 x 4 over 300, 64 dims 15.2 | 9.8, 128 dims 19.3 | 12.1.  (With many items of 64 dims the idle
+// 16.7 | 29.2, 1 x 448 30.9 | 34.5, 4 x 200 44.2 | 35.5.  8 heads: 1 x 64 over 8000, 64 dims 24.7 | 107, 128 dims
+// 28.7 | 129; 1 x 4 over 300, 64 dims 15.2 | 9.8, 128 dims 19.3 | 12.1.  (With many items of 64 dims the idle
 // CTAs of the last round are no loss: two CTAs an SM slow one another.)
 int cross_ws_slices(int32_t num_seqs, int32_t num_kv_heads, int32_t group, int32_t head_dim, int32_t max_q_len,
                     int64_t max_len) {
