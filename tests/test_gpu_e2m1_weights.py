@@ -7,6 +7,8 @@ one, x = 36 in the decode kernel (weights times 2^11) and 32 in the prefill tile
 2^-24 either way; the products' sums in fp32 (n / 16 steps of at most 2^-23: 2^-10); scores of up to 30 in
 fp32 (2^-18).
 """
+import functools
+
 import numpy as np
 import pytest
 import torch
@@ -27,17 +29,23 @@ def h():
     return gpu_harness
 
 
+@functools.lru_cache(maxsize=1)
+def pools(heads, d, at):
+    """The 4-bit pools, and their values as bf16 pools."""
+    rng = np.random.default_rng(heads + d)
+    codes = np.zeros((N // BS, heads, BS, d), dtype=np.uint8)
+    scales = np.full((N // BS, heads, BS, d // 16), 0x38, dtype=np.uint8)          # 1.0
+    vcodes = rng.integers(1, 8, codes.shape).astype(np.uint8)
+    codes[at // BS, :, at % BS], vcodes[at // BS, :, at % BS] = 2, 0               # 1.0; zero
+    bits = e2m1.bf16_bits(e2m1.MAGNITUDES)
+    return [e2m1.pack(x, scales) for x in (codes, vcodes)], [bits[x] for x in (codes, vcodes)]
+
+
 class Sink:
     """One sequence's blocks in order; q all ones, K zero but the sink's, a score of gap ln 2."""
 
     def __init__(self, heads, d, gap, at, seqs, small=2.0 ** -36):
-        rng = np.random.default_rng(heads + d)
-        codes = np.zeros((N // BS, heads, BS, d), dtype=np.uint8)
-        scales = np.full((N // BS, heads, BS, d // 16), 0x38, dtype=np.uint8)      # 1.0
-        vcodes = rng.integers(1, 8, codes.shape).astype(np.uint8)
-        codes[at // BS, :, at % BS], vcodes[at // BS, :, at % BS] = 2, 0           # 1.0; zero
-        self.pools = [e2m1.pack(codes, scales), e2m1.pack(vcodes, scales)]
-        values = [e2m1.bf16_bits(e2m1.values(x, scales)) for x in (codes, vcodes)]
+        self.pools, values = pools(heads, d, at)
         self.scale = float(np.float32(gap * np.log(2.0) / d))
         self.q = np.full((seqs, heads, d), 0x3F80, dtype=np.uint16)
         self.table = np.arange(N // BS, dtype=np.int32)[None]
@@ -58,9 +66,8 @@ class Sink:
         assert err.max() <= 0, "outside the tolerance by %g, the largest output %g" % (err.max(), self.ref.max())
 
 
-@pytest.mark.parametrize("gap", [24.5, 25.5, 30.0])
-@pytest.mark.parametrize("at", [0, N - 1])
-@pytest.mark.parametrize("d", [64, 128])
+# (the pools of one (d, at) are made once for the gaps)
+@pytest.mark.parametrize("d,at,gap", [(d, at, gap) for d in (64, 128) for at in (0, N - 1) for gap in (24.5, 25.5, 30.0)])
 def test_decode(h, d, at, gap):
     c = Sink(8, d, gap, at, 1)
     opts = pa.DecodeOptions(kv_dtype=pa.PA_KV_E2M1, k_scale=1.0, v_scale=1.0, max_ctas=1, flags=pa.PA_FLAG_CHECK)
@@ -71,9 +78,8 @@ def test_decode(h, d, at, gap):
     c.check(out)
 
 
-@pytest.mark.parametrize("gap", [24.5, 25.5, 30.0])
-@pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("kernel", [pa.PA_PREFILL_ROWS, pa.PA_PREFILL_TCGEN05_WS])
+@pytest.mark.parametrize("kernel,d,gap", [(k, d, gap) for k in (pa.PA_PREFILL_ROWS, pa.PA_PREFILL_TCGEN05_WS)
+                                          for d in (64, 128) for gap in (24.5, 25.5, 30.0)])
 def test_prefill(h, kernel, d, gap):
     # one row a sequence, the sequences over the same blocks: as many items as SMs, so that none is cut
     if kernel == pa.PA_PREFILL_TCGEN05_WS:
