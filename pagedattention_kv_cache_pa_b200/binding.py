@@ -224,16 +224,16 @@ def _dev(t, dtype_name: str, what: str):
 
 
 def _cache(t, desc: "CacheDesc", what: str, options=None):
-    """Device pointer of a KV cache tensor (bf16, or uint8 E4M3 codes or 4-bit pages when the
-    options say so) that holds at least the pool desc describes."""
+    """Device pointer of a KV cache tensor (bf16, or uint8 E4M3 codes when the options say so) that
+    holds at least the pool desc describes."""
     kv_dtype = PA_KV_BF16 if options is None else options.kv_dtype
-    if t is not None and not isinstance(t, int):
-        need = _pool_elements(desc, kv_dtype)
-        if t.numel() < need:
-            raise ValueError("%s holds %d elements, the pool described needs %d" % (what, t.numel(), need))
-    if kv_dtype == PA_KV_E2M1:
-        return _here(t, "uint8", what, _device())
-    return _dev(t, "bfloat16" if kv_dtype == PA_KV_BF16 else "uint8", what)
+    return _pool(t, "bfloat16" if kv_dtype == PA_KV_BF16 else "uint8", what, _pool_elements(desc, kv_dtype))
+
+
+def _pool(t, dtype_name: str, what: str, need: int):
+    if t is not None and not isinstance(t, int) and t.numel() < need:
+        raise ValueError("%s holds %d elements, the pool described needs %d" % (what, t.numel(), need))
+    return _dev(t, dtype_name, what)
 
 
 def _here(t, dtype_name: str, what: str, device: int, need: int = 0):
@@ -252,30 +252,35 @@ def _here(t, dtype_name: str, what: str, device: int, need: int = 0):
     return ptr
 
 
-def _sized(t, dtype_name: str, what: str, device, need: int):
-    """_here for a call over 4-bit pools; for the other types (device None) _dev."""
-    return _dev(t, dtype_name, what) if device is None else _here(t, dtype_name, what, device, need)
-
-
-def _decode_sizes(desc: "CacheDesc", options, n: int):
-    """(current device, elements of q and out, of a new K or V, of the tables) of a decode of n sequences
-    over 4-bit pools; (None, 0, 0, 0) over others."""
-    if options is None or options.kv_dtype != PA_KV_E2M1:
-        return None, 0, 0, 0
-    row = n * desc.head_dim
-    return _device(), row * desc.num_q_heads, row * desc.num_kv_heads, n * desc.max_blocks_per_seq
-
-
-def _scratch(t, device):
-    """Device pointer of a workspace of any type (or a raw int); over 4-bit pools it is of this device."""
-    if isinstance(t, int):
-        return t
-    if device is not None:
-        if t.get_device() != device:
-            raise ValueError("workspace is on %s, the current device is cuda:%d" % (t.device, device))
-        if not t.is_contiguous():
+def _decode_pointers(q, k, v, k_cache, v_cache, block_tables, context_lens, out, workspace, n: int, desc: "CacheDesc",
+                     options):
+    """Device pointers of a decode's tensors (k, v, workspace: None where the call has none), which the caller
+    keeps until the library's call returns.  Over 4-bit pools each is held to the current device and to the
+    size that the call names."""
+    kv_dtype = PA_KV_BF16 if options is None else options.kv_dtype
+    dim, heads = desc.head_dim, desc.num_kv_heads
+    pool = desc.num_blocks * heads * desc.block_size * dim
+    if kv_dtype != PA_KV_E2M1:
+        cache = "bfloat16" if kv_dtype == PA_KV_BF16 else "uint8"
+        if k is not None or v is not None:
+            k, v = _dev(k, "bfloat16", "k"), _dev(v, "bfloat16", "v")
+        ws = workspace if workspace is None or isinstance(workspace, int) else workspace.data_ptr()
+        return (_dev(q, "bfloat16", "q"), k, v, _pool(k_cache, cache, "k_cache", pool),
+                _pool(v_cache, cache, "v_cache", pool), _dev(block_tables, "int32", "block_tables"),
+                _dev(context_lens, "int32", "context_lens"), _dev(out, "bfloat16", "out"), ws)
+    at, rows, pool = _device(), n * dim * desc.num_q_heads, pool * 9 // 16
+    if k is not None or v is not None:
+        k, v = _here(k, "bfloat16", "k", at, n * dim * heads), _here(v, "bfloat16", "v", at, n * dim * heads)
+    if workspace is not None and not isinstance(workspace, int):   # of any type
+        if workspace.get_device() != at:
+            raise ValueError("workspace is on %s, the current device is cuda:%d" % (workspace.device, at))
+        if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
-    return t.data_ptr()
+        workspace = workspace.data_ptr()
+    return (_here(q, "bfloat16", "q", at, rows), k, v, _here(k_cache, "uint8", "k_cache", at, pool),
+            _here(v_cache, "uint8", "v_cache", at, pool),
+            _here(block_tables, "int32", "block_tables", at, n * desc.max_blocks_per_seq),
+            _here(context_lens, "int32", "context_lens", at, n), _here(out, "bfloat16", "out", at, rows), workspace)
 
 
 def _elements(t) -> int:
@@ -544,14 +549,9 @@ def pa_decode(q, k_cache, v_cache, block_tables, context_lens, max_context_len: 
               num_seqs: int | None = None, workspace_bytes: int | None = None) -> None:
     n = int(context_lens.shape[0]) if num_seqs is None else int(num_seqs)
     wbytes = workspace.numel() * workspace.element_size() if workspace_bytes is None else int(workspace_bytes)
-    at, rows, _, tables = _decode_sizes(desc, options, n)
-    _check(lib.pa_decode_ex(_sized(q, "bfloat16", "q", at, rows), _cache(k_cache, desc, "k_cache", options),
-                            _cache(v_cache, desc, "v_cache", options),
-                            _sized(block_tables, "int32", "block_tables", at, tables),
-                            _sized(context_lens, "int32", "context_lens", at, n), n, int(max_context_len),
-                            float(scale), _sized(out, "bfloat16", "out", at, rows), _scratch(workspace, at), wbytes,
-                            ctypes.byref(desc),
-                            ctypes.byref(options) if options is not None else None,
+    p = _decode_pointers(q, None, None, k_cache, v_cache, block_tables, context_lens, out, workspace, n, desc, options)
+    _check(lib.pa_decode_ex(p[0], p[3], p[4], p[5], p[6], n, int(max_context_len), float(scale), p[7], p[8], wbytes,
+                            ctypes.byref(desc), ctypes.byref(options) if options is not None else None,
                             _stream(stream)), "pa_decode")
 
 
@@ -562,16 +562,10 @@ def pa_append_decode(q, k, v, k_cache, v_cache, block_tables, context_lens, max_
     """Append each sequence's newest token at position context_lens-1, then decode."""
     n = int(context_lens.shape[0]) if num_seqs is None else int(num_seqs)
     wbytes = workspace.numel() * workspace.element_size() if workspace_bytes is None else int(workspace_bytes)
-    at, rows, new, tables = _decode_sizes(desc, options, n)
-    _check(lib.pa_append_decode(_sized(q, "bfloat16", "q", at, rows), _sized(k, "bfloat16", "k", at, new),
-                                _sized(v, "bfloat16", "v", at, new), _cache(k_cache, desc, "k_cache", options),
-                                _cache(v_cache, desc, "v_cache", options),
-                                _sized(block_tables, "int32", "block_tables", at, tables),
-                                _sized(context_lens, "int32", "context_lens", at, n), n,
-                                int(max_context_len), float(scale), _sized(out, "bfloat16", "out", at, rows),
-                                _scratch(workspace, at), wbytes, ctypes.byref(desc),
-                                ctypes.byref(options) if options is not None else None,
-                                _stream(stream)), "pa_append_decode")
+    p = _decode_pointers(q, k, v, k_cache, v_cache, block_tables, context_lens, out, workspace, n, desc, options)
+    _check(lib.pa_append_decode(*p[:7], n, int(max_context_len), float(scale), p[7], p[8], wbytes, ctypes.byref(desc),
+                                ctypes.byref(options) if options is not None else None, _stream(stream)),
+           "pa_append_decode")
 
 
 def pa_decode_noalloc(q, k_cache, v_cache, block_tables, context_lens, max_context_len: int,
@@ -579,14 +573,9 @@ def pa_decode_noalloc(q, k_cache, v_cache, block_tables, context_lens, max_conte
                       stream=None, num_seqs: int | None = None) -> None:
     """pa_decode with the library's fixed scratch array instead of a caller workspace."""
     n = int(context_lens.shape[0]) if num_seqs is None else int(num_seqs)
-    at, rows, _, tables = _decode_sizes(desc, options, n)
-    _check(lib.pa_decode_noalloc(_sized(q, "bfloat16", "q", at, rows), _cache(k_cache, desc, "k_cache", options),
-                                 _cache(v_cache, desc, "v_cache", options),
-                                 _sized(block_tables, "int32", "block_tables", at, tables),
-                                 _sized(context_lens, "int32", "context_lens", at, n), n,
-                                 int(max_context_len), float(scale), _sized(out, "bfloat16", "out", at, rows),
-                                 ctypes.byref(desc),
-                                 ctypes.byref(options) if options is not None else None,
+    p = _decode_pointers(q, None, None, k_cache, v_cache, block_tables, context_lens, out, None, n, desc, options)
+    _check(lib.pa_decode_noalloc(p[0], p[3], p[4], p[5], p[6], n, int(max_context_len), float(scale), p[7],
+                                 ctypes.byref(desc), ctypes.byref(options) if options is not None else None,
                                  _stream(stream)), "pa_decode_noalloc")
 
 
