@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::kMinBlocks)
     const int q0 = p.cu_q[b], Tq = p.cu_q[b + 1] - q0;
     const int L = p.context_lens[b];
     if (Tq <= 0) return;
-    if (L < Tq || L > p.len_cap || Tq > p.max_q_len) {             // fewer tokens than queries, past the table,
+    if (L < Tq || L > p.len_cap || Tq > p.max_q_len) {       // fewer tokens than queries, past the table,
                                                              // or more queries than the grid holds
         if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) raise_status(p.status, kStatusBadLength);
         return;

@@ -860,8 +860,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int h = 0; h < D / 32; ++h) {
                 uint32_t o[32];
                 tmem_ld32(t_o + h * 32, o);                  // warp-wide: padded rows join the load
-                // V's scale only after the division: a small one over a long context's sum is no float.  (By
-                // pairs: one by one, the 1021 rows of 15000 took 640 us for 630.)
+                // V's scale only after the division: a small one over a long context's sum is no float
 #pragma unroll
                 for (int j = 0; j < 32; j += 2) {
                     uint64_t y = f2_mul(f2(__uint_as_float(o[j]), __uint_as_float(o[j + 1])), f2(inv, inv));
