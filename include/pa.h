@@ -377,8 +377,8 @@ PA_API int pa_prefill(const pa_bf16* q, const pa_bf16* k_cache, const pa_bf16* v
  * pa_prefill over a bf16 or a 4-bit cache.  options (NULL: all zero): kernel as for
  * pa_prefill; kv_dtype PA_KV_BF16 or PA_KV_E2M1 (4-bit pools, see pa_append_kv_e2m1, with
  * their scales, scale * k_scale * log2(e) a finite float; block sizes of 4-bit pools;
- * kernel PA_PREFILL_TCGEN05_WS: tiles of 256 query rows; PA_PREFILL_ROWS: the decode kernel with several rows' heads for its columns, Hq / Hkv <= 16;
- * PA_PREFILL_AUTO: the latter for few rows).
+ * kernel PA_PREFILL_TCGEN05_WS: tiles of 256 query rows; PA_PREFILL_ROWS: the decode kernel with
+ * several rows' heads for its columns, Hq / Hkv <= 16; PA_PREFILL_AUTO: the latter for few rows).
  * 4-bit K is widened to bf16 (rows: f16, as q is after a power of two per row) and V to f16
  * exactly, P is rounded to f16 as pa_decode's is (tiles: by 2^-12 down to 2^-21 of the row's largest
  * weight, by 2^-32 of that below).  A NaN held in V may also reach rows before its token (P is 0
